@@ -190,6 +190,85 @@ pw_status pw_moe_forward_noalloc(pw_ctx* ctx, const void* x, const float* logits
 pw_status pw_route(pw_ctx* ctx, const float* logits, int32_t T, int32_t* ids, float* g,
                    int32_t* counts, void* stream);
 
+/* ---- Around the expert layer: gated routing, given routes, dense products ---- */
+
+/* Element types of the tensors these calls take. */
+typedef enum { PW_F32 = 0, PW_F16 = 1, PW_BF16 = 2 } pw_dtype;
+
+typedef enum { PW_SCORE_SOFTMAX = 0, PW_SCORE_SIGMOID = 1 } pw_score;
+
+typedef struct {
+    int32_t score;        /* pw_score                                             */
+    int32_t n_group;      /* G groups of E / G consecutive experts; 1: no groups  */
+    int32_t topk_group;   /* groups that stay, 1 .. n_group                       */
+    int32_t group_top2;   /* a group's score: 0 its largest choice score,
+                             1 the sum of its two largest                         */
+    int32_t renorm;       /* 0: weight = score; 1: score over the chosen's sum    */
+    float scale;          /* the weights are multiplied by it                     */
+} pw_gate_desc;
+
+/* Gated routing of T tokens over the layer's experts, top_k of ctx (its
+ * renorm is not used). logits [T, E] of logits_dtype (pw_dtype), rows
+ * ld_logits elements apart (>= E); bias fp32 [E] or NULL; mask [T] bytes or
+ * NULL (0: a padded token, its logits are not read). An expert is to be had
+ * by a token unless its logit is NaN, -inf or the type's lowest finite
+ * value. With s its score (softmax over the experts to be had, or sigmoid)
+ * and c = s + bias: the topk_group best groups stay (ties: lower group),
+ * and of their experts the top_k with the largest c are chosen, in that
+ * order (ties: lower expert; an expert whose c is NaN or -inf is not
+ * chosen). The bias counts in the choice only. The choice is that of the
+ * scores in fp64, also where fp32 could not tell two apart. Out: ids int32 [T, k] (-1 in slots left over), g fp32
+ * [T, k] (0 there; renormalised weights over an empty choice are 0) and
+ * counts int32 [E] (pairs per expert; may be NULL). 0 <= T <= max_tokens;
+ * n_group <= 64 divides E, topk_group E / n_group >= top_k, scale finite.
+ * T = 0 only clears counts. Needs neither pages nor a workspace, does not
+ * synchronise, and can be captured and replayed. */
+pw_status pw_route_gated(pw_ctx* ctx, const pw_gate_desc* gate, const void* logits, int32_t logits_dtype,
+                         int64_t ld_logits, const float* bias, const uint8_t* mask, int32_t T, int32_t* ids,
+                         float* g, int32_t* counts, void* stream);
+
+/* Forward pass for given routes: x bf16 [T, d], ids int32 [T, k] and g fp32
+ * [T, k] as pw_route or pw_route_gated write them;
+ * y_t = residual_t + sum_j g_tj W2 (silu(W1 x_t) * (W3 x_t)) over the slots
+ * with an expert. An id outside [0, E) is a slot without one (its weight is
+ * not used); an expert named twice by a token counts with both weights.
+ * residual (NULL: none) and y [T, d] have type y_dtype, PW_F32 or PW_BF16;
+ * residual may be y itself. Rounded once, to y's type; accuracy as
+ * pw_moe_forward. 16-byte aligned x, y and residual. Works in the bound
+ * workspace; records only kernel launches and clears its own counters, so a
+ * captured call can be replayed (with a host tier as well). */
+pw_status pw_moe_forward_routed(pw_ctx* ctx, const void* x, const int32_t* ids, const float* g, int32_t T,
+                                const void* residual, void* y, int32_t y_dtype, void* stream);
+
+/* Epilogue of pw_linear: f(z) of the sum z = x w^T + bias. GELU is z Phi(z),
+ * GELU_TANH its tanh form. SWIGLU: w has 2 N rows, the N gate rows and then
+ * the N up rows (bias [2 N] alike), f = silu(z_gate) z_up. */
+typedef enum {
+    PW_ACT_NONE = 0, PW_ACT_RELU = 1, PW_ACT_SILU = 2, PW_ACT_SIGMOID = 3,
+    PW_ACT_GELU = 4, PW_ACT_GELU_TANH = 5, PW_ACT_SWIGLU = 6
+} pw_act;
+
+typedef struct {
+    int32_t M, N, K;      /* y [M, N] from x [M, K] and w [N, K] (SWIGLU: [2 N, K]) */
+    int32_t in_dtype;     /* of x and w: PW_BF16 or PW_F16                          */
+    int32_t out_dtype;    /* of y and residual                                      */
+    int32_t act;          /* pw_act                                                 */
+    int64_t ldx, ldw;     /* elements between rows of x (>= K), w (>= K),           */
+    int64_t ldr, ldy;     /* residual (>= N) and y (>= N)                           */
+} pw_linear_desc;
+
+/* Dense product (router logits, shared experts): y = f(x w^T + bias) +
+ * residual. bias fp32 or NULL, residual or NULL (it may be y itself, with
+ * ldr = ldy); every pointer aligned to its element, y not overlapping x or
+ * w. Operands are multiplied exactly and summed in fp32; everything after
+ * in fp32, rounded once. Rows of x and w of any alignment and length
+ * (16-byte aligned ones, with K a multiple of 8, are faster); ldx and ldw
+ * below 2^22 where the tensor has more than one row. M = 0 or N = 0 does
+ * nothing, K = 0 gives f(bias) + residual. Host checks only, no workspace,
+ * no synchronisation; can be captured. Uses the current device. */
+pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
+                    const void* residual, void* y, void* stream);
+
 /* Host copy of the page table (entries [E]). */
 pw_status pw_get_page_table(const pw_ctx* ctx, pw_page_entry* out);
 

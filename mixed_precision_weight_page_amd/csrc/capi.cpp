@@ -192,7 +192,9 @@ struct WsView {
 
 WsView bound_ws(const pw_ctx* c) { return WsView{c->ws, c->lay, c->desc.max_tokens, c->nsplit}; }
 
-// The forward scratch of a view; `parity` picks the grouping counter set.
+// The forward scratch of a view; `parity` picks the grouping counter set
+// (0, 1: the sets that alternate; 2: the one of given routes, set 3 its
+// never read counterpart).
 FwdWork fwd_work(const pw_ctx* c, const WsView& v, int parity) {
     FwdWork w;
     uint8_t* b = v.base;
@@ -208,7 +210,7 @@ FwdWork fwd_work(const pw_ctx* c, const WsView& v, int parity) {
     w.tiles = reinterpret_cast<TileDesc*>(b + L.tiles);
     // the two counter sets: cnt [E], act [E], n_act [2], each set 256-byte aligned
     auto set = [&](int i) {
-        uint8_t* q = b + L.dg + (uint64_t)i * (L.dg_bytes / 2);
+        uint8_t* q = b + (i < 2 ? L.dg : L.rg) + (uint64_t)(i & 1) * (L.dg_bytes / 2);
         DecodeGroup g;
         g.cnt = reinterpret_cast<int32_t*>(q);
         g.act = g.cnt + c->E;
@@ -218,7 +220,7 @@ FwdWork fwd_work(const pw_ctx* c, const WsView& v, int parity) {
         return g;
     };
     w.dg = set(parity);
-    w.dg_next = set(1 - parity);
+    w.dg_next = set(parity ^ 1);
     w.tcap = std::max(v.max_tokens, 16);
     w.ccnt = reinterpret_cast<int32_t*>(b + L.ccnt);
     w.cpre = reinterpret_cast<int32_t*>(b + L.cpre);
@@ -518,7 +520,8 @@ Layout workspace_layout(int E, int d, int F, int k, int max_tokens, int nsplit) 
     // everything the statistics pass may overwrite
     L.dg_bytes = 2 * align_up(4 * (2 * (uint64_t)E + 2), kAlign);
     L.dg = std::max(L.fwd_end, L.stats_end);
-    L.total = L.dg + L.dg_bytes;
+    L.rg = L.dg + L.dg_bytes;
+    L.total = L.rg + L.dg_bytes;
     return L;
 }
 }  // namespace pw
@@ -826,6 +829,37 @@ static pw_status route_batch(pw_ctx* c, const WsView& v, const FwdWork& w, const
     return PW_OK;
 }
 
+// Routes a caller gives to pw_moe_forward_routed.
+struct GivenRoutes {
+    const int32_t* ids;
+    const float* g;
+    const void* residual;
+    int y_dtype;
+};
+
+// Given routes into the scratch, grouped for the path of the batch. The
+// counter set of these calls is cleared at each of them, so that neither a
+// replayed graph nor a forward between replays finds another's counts.
+static pw_status accept_batch(pw_ctx* c, const WsView& v, const FwdWork& w, const GivenRoutes& r, const void* x,
+                              int32_t T, bool dense, hipStream_t s, KTimer t, const int32_t** counts, int own_route) {
+    RouteArgs ra{nullptr, static_cast<const uint16_t*>(x), c->d, T, c->E, c->k, c->desc.renorm, 1,
+                 bitplane(c) ? dev_table(c, c->cur).bits : nullptr};
+    if (dense) {
+        ra.x = nullptr;   // prep_x takes the statistics on this path
+        ra.group = 0;
+        HIP_TRY(c, launch_accept_routes(ra, w, r.ids, r.g, s, t));
+        HIP_TRY(c, launch_group_pairs(ra, w, dev_table(c, c->cur), s));
+        *counts = w.cnt;
+        return PW_OK;
+    }
+    ra.group = own_route ? 0 : 1;
+    if (ra.group)
+        HIP_TRY(c, launch_zero_i32(reinterpret_cast<int32_t*>(v.base + v.lay.rg), v.lay.dg_bytes / 8, s));
+    HIP_TRY(c, launch_accept_routes(ra, w, r.ids, r.g, s, t));
+    *counts = w.dg.cnt;
+    return PW_OK;
+}
+
 static pw_status forward_checks(pw_ctx* c, const void* logits, int32_t T) {
     if (T < 0 || T > c->desc.max_tokens)
         return fail(c, PW_ERR_INVALID_ARG, "T = %d outside [0, %d]", T, c->desc.max_tokens);
@@ -859,8 +893,8 @@ pw_status pw_route(pw_ctx* c, const float* logits, int32_t T, int32_t* ids, floa
 // SwiGLU, down, combine). `scratch`: the view is the static scratch (no
 // timing events, counters cleared at each call).
 static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const float* logits, int32_t T,
-                              float* y, hipStream_t s, bool scratch) {
-    const FwdWork w = fwd_work(c, v, scratch ? 0 : c->dg_parity);
+                              void* y, hipStream_t s, bool scratch, const GivenRoutes* given = nullptr) {
+    const FwdWork w = fwd_work(c, v, given ? 2 : (scratch ? 0 : c->dg_parity));
     KTimer tm[4];
     if (c->profile_mask && !scratch) {
         for (int j = 0; j < 4; ++j) {
@@ -876,9 +910,11 @@ static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const f
     const bool dense = dense_path(c, T);
     // small decode batches are routed by the gate/up kernel itself (not with
     // a host tier: its plan needs the counts before the expert kernels)
-    const int own_route = (!dense && !swap_mode(c)) ? own_route_mode(T, c->E, c->k) : 0;
+    int own_route = (!dense && !swap_mode(c)) ? own_route_mode(T, c->E, c->k) : 0;
+    if (given && own_route) own_route = 2;   // nothing to route: it groups the given ids
     const int32_t* cnt = nullptr;
-    pw_status st = route_batch(c, v, w, logits, x, T, dense, scratch, s, tm[0], &cnt, own_route);
+    pw_status st = given ? accept_batch(c, v, w, *given, x, T, dense, s, tm[0], &cnt, own_route)
+                         : route_batch(c, v, w, logits, x, T, dense, scratch, s, tm[0], &cnt, own_route);
     if (st != PW_OK) return st;
     // pages: pool + offset, or with a host tier the addresses of this pass
     // (slot or host tier) after the missing pages are copied in
@@ -896,6 +932,10 @@ static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const f
     // batch's pair count as the split stride, so a view sized for large
     // batches splits small ones as far as its buffer allows
     const int P = (int)pairs;
+    auto combine = [&](int nsplit) {
+        return given ? launch_combine_routed(w, T, c->d, c->k, P, nsplit, given->residual, y, given->y_dtype, s, tm[3])
+                     : launch_combine(w, T, c->d, c->k, P, nsplit, static_cast<float*>(y), s, tm[3]);
+    };
     if (dense) {
         GemmArgs ga;
         ga.pool = base;
@@ -915,7 +955,7 @@ static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const f
         HIP_TRY(c, launch_prep_x(ga, s));
         HIP_TRY(c, launch_gate_up_gemm(ga, s, tm[1]));
         HIP_TRY(c, launch_down_gemm(ga, s, tm[2]));
-        HIP_TRY(c, launch_combine(w, T, c->d, c->k, P, 1, y, s, tm[3]));
+        HIP_TRY(c, combine(1));
     } else {
         FfnArgs fa;
         fa.pool = base;
@@ -940,13 +980,13 @@ static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const f
         const int nsplit = down_splits(c->F, c->d, max_act, (int)std::min<int64_t>(cap_pairs / pairs, 1 << 30));
         HIP_TRY(c, launch_gate_up(fa, plan_ffn(c->d, T, 1), s, tm[1]));
         HIP_TRY(c, launch_down(fa, plan_ffn(c->F, T, nsplit), s, tm[2]));
-        HIP_TRY(c, launch_combine(w, T, c->d, c->k, P, nsplit, y, s, tm[3]));
+        HIP_TRY(c, combine(nsplit));
     }
     if (c->profile_mask && !scratch) c->forwards_timed++;
     return PW_OK;
 }
 
-static pw_status forward_args(pw_ctx* c, const void* x, const float* logits, int32_t T, const float* y) {
+static pw_status forward_args(pw_ctx* c, const void* x, int32_t T, const void* y) {
     if (!c->pages_valid) return fail(c, PW_ERR_STATE, "no quantized pages: call pw_quantize_experts or pw_set_budget first");
     if (T == 0) return PW_OK;
     if (!x || !y) return fail(c, PW_ERR_INVALID_ARG, "null x or y");
@@ -960,7 +1000,7 @@ pw_status pw_moe_forward(pw_ctx* c, const void* x, const float* logits, int32_t 
     if (!c) return PW_ERR_INVALID_ARG;
     pw_status st = forward_checks(c, logits, T);
     if (st != PW_OK) return st;
-    if ((st = forward_args(c, x, logits, T, y)) != PW_OK || T == 0) return st;
+    if ((st = forward_args(c, x, T, y)) != PW_OK || T == 0) return st;
     if ((st = ensure_device(c)) != PW_OK) return st;
     return forward_core(c, bound_ws(c), x, logits, T, y, static_cast<hipStream_t>(stream), false);
 }
@@ -971,7 +1011,7 @@ pw_status pw_moe_forward_noalloc(pw_ctx* c, const void* x, const float* logits, 
     if (T < 0 || T > c->desc.max_tokens)
         return fail(c, PW_ERR_INVALID_ARG, "T = %d outside [0, %d]", T, c->desc.max_tokens);
     if (T > 0 && !logits) return fail(c, PW_ERR_INVALID_ARG, "null logits");
-    pw_status st = forward_args(c, x, logits, T, y);
+    pw_status st = forward_args(c, x, T, y);
     if (st != PW_OK || T == 0) return st;
     // the device state exists once pages do; ensure_device then only checks
     // that the context's device is current
@@ -997,6 +1037,121 @@ pw_status pw_moe_forward_noalloc(pw_ctx* c, const void* x, const float* logits, 
         return fail(c, PW_ERR_HIP, "hipGetSymbolAddress of the static scratch failed on device %d", c->device);
     v.base = static_cast<uint8_t*>(p);
     return forward_core(c, v, x, logits, T, y, static_cast<hipStream_t>(stream), true);
+}
+
+pw_status pw_moe_forward_routed(pw_ctx* c, const void* x, const int32_t* ids, const float* g, int32_t T,
+                                const void* residual, void* y, int32_t y_dtype, void* stream) {
+    if (!c) return PW_ERR_INVALID_ARG;
+    if (T < 0 || T > c->desc.max_tokens)
+        return fail(c, PW_ERR_INVALID_ARG, "T = %d outside [0, %d]", T, c->desc.max_tokens);
+    if (y_dtype != PW_F32 && y_dtype != PW_BF16) return fail(c, PW_ERR_INVALID_ARG, "y must be fp32 or bf16");
+    if (T > 0 && (!ids || !g)) return fail(c, PW_ERR_INVALID_ARG, "null ids or g");
+    if (T > 0 && ((uintptr_t)ids % 4 || (uintptr_t)g % 4 || (uintptr_t)residual % 16))
+        return fail(c, PW_ERR_INVALID_ARG, "ids and g must be 4-byte and residual 16-byte aligned");
+    if (!c->ws) return fail(c, PW_ERR_WORKSPACE, "no workspace bound");
+    pw_status st = forward_args(c, x, T, y);
+    if (st != PW_OK || T == 0) return st;
+    if ((st = ensure_device(c)) != PW_OK) return st;
+    const GivenRoutes given{ids, g, residual, y_dtype};
+    return forward_core(c, bound_ws(c), x, nullptr, T, y, static_cast<hipStream_t>(stream), false, &given);
+}
+
+static uintptr_t elem_bytes(int32_t dtype) { return dtype == PW_F32 ? 4 : 2; }
+static bool dtype_ok(int32_t dtype) { return dtype == PW_F32 || dtype == PW_F16 || dtype == PW_BF16; }
+
+pw_status pw_route_gated(pw_ctx* c, const pw_gate_desc* gate, const void* logits, int32_t logits_dtype,
+                         int64_t ld_logits, const float* bias, const uint8_t* mask, int32_t T, int32_t* ids,
+                         float* g, int32_t* counts, void* stream) {
+    if (!c) return PW_ERR_INVALID_ARG;
+    if (!gate) return fail(c, PW_ERR_INVALID_ARG, "null gate description");
+    const pw_gate_desc& d = *gate;
+    if (T < 0 || T > c->desc.max_tokens)
+        return fail(c, PW_ERR_INVALID_ARG, "T = %d outside [0, %d]", T, c->desc.max_tokens);
+    if (d.score != PW_SCORE_SOFTMAX && d.score != PW_SCORE_SIGMOID)
+        return fail(c, PW_ERR_INVALID_ARG, "unknown score %d", d.score);
+    if (d.n_group < 1 || d.n_group > 64 || c->E % d.n_group)
+        return fail(c, PW_ERR_INVALID_ARG, "n_group = %d must divide %d experts and be at most 64", d.n_group, c->E);
+    if (d.topk_group < 1 || d.topk_group > d.n_group || d.topk_group * (c->E / d.n_group) < c->k)
+        return fail(c, PW_ERR_INVALID_ARG, "%d of %d groups of %d experts cannot hold top-%d", d.topk_group, d.n_group,
+                    c->E / d.n_group, c->k);
+    if ((d.group_top2 != 0 && d.group_top2 != 1) || (d.renorm != 0 && d.renorm != 1) || !std::isfinite(d.scale))
+        return fail(c, PW_ERR_INVALID_ARG, "group_top2 and renorm must be 0 or 1, scale finite");
+    if (!dtype_ok(logits_dtype)) return fail(c, PW_ERR_INVALID_ARG, "unknown logits type %d", logits_dtype);
+    if (T > 1 && ld_logits < c->E)
+        return fail(c, PW_ERR_INVALID_ARG, "rows of %d logits %lld elements apart", c->E, (long long)ld_logits);
+    if (T > 0 && (!logits || !ids || !g)) return fail(c, PW_ERR_INVALID_ARG, "null logits, ids or g");
+    if ((uintptr_t)logits % elem_bytes(logits_dtype) || (uintptr_t)bias % 4 || (uintptr_t)ids % 4 ||
+        (uintptr_t)g % 4 || (uintptr_t)counts % 4)
+        return fail(c, PW_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    if (c->dev) {   // the layer's device, once it has one
+        pw_status st = ensure_device(c);
+        if (st != PW_OK) return st;
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        if (counts) HIP_TRY(c, launch_zero_i32(counts, (uint64_t)c->E, s));
+        return PW_OK;
+    }
+    GateArgs a{};
+    a.logits = logits;
+    a.ld = ld_logits;
+    a.dtype = logits_dtype;
+    a.bias = bias;
+    a.mask = mask;
+    a.T = T;
+    a.E = c->E;
+    a.k = c->k;
+    a.score = d.score;
+    a.n_group = d.n_group;
+    a.topk_group = d.topk_group;
+    a.group_top2 = d.group_top2;
+    a.renorm = d.renorm;
+    a.scale = d.scale;
+    a.ids = ids;
+    a.g = g;
+    a.counts = counts;
+    HIP_TRY(c, launch_gate(a, s));
+    return PW_OK;
+}
+
+pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
+                    const void* residual, void* y, void* stream) {
+    if (!desc) return PW_ERR_INVALID_ARG;
+    const pw_linear_desc& d = *desc;
+    if (d.M < 0 || d.N < 0 || d.K < 0 || d.N > (1 << 30) || d.K > (1 << 29)) return PW_ERR_INVALID_ARG;
+    if ((d.in_dtype != PW_BF16 && d.in_dtype != PW_F16) || !dtype_ok(d.out_dtype)) return PW_ERR_INVALID_ARG;
+    if (d.act < PW_ACT_NONE || d.act > PW_ACT_SWIGLU) return PW_ERR_INVALID_ARG;
+    if (d.M == 0 || d.N == 0) return PW_OK;
+    LinearArgs a{};
+    const bool glu = d.act == PW_ACT_SWIGLU;
+    const int64_t rows = glu ? 2 * (int64_t)d.N : d.N;
+    // a single row has no distance to a next one
+    a.ldx = d.M > 1 ? d.ldx : d.K;
+    a.ldw = rows > 1 ? d.ldw : d.K;
+    a.ldr = d.M > 1 ? d.ldr : d.N;
+    a.ldy = d.M > 1 ? d.ldy : d.N;
+    constexpr int64_t kMaxLd = (int64_t)1 << 22;   // 256 rows of a tile within a 31-bit byte offset
+    if (a.ldx < d.K || a.ldw < d.K || a.ldy < d.N || (residual && a.ldr < d.N)) return PW_ERR_INVALID_ARG;
+    if ((d.M > 1 && a.ldx >= kMaxLd) || (rows > 1 && a.ldw >= kMaxLd)) return PW_ERR_INVALID_ARG;
+    if (!y || (d.K > 0 && (!x || !w))) return PW_ERR_INVALID_ARG;
+    const uintptr_t ob = elem_bytes(d.out_dtype);
+    if ((uintptr_t)x % 2 || (uintptr_t)w % 2 || (uintptr_t)bias % 4 || (uintptr_t)residual % ob || (uintptr_t)y % ob)
+        return PW_ERR_INVALID_ARG;
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.M = d.M;
+    a.N = d.N;
+    a.K = d.K;
+    a.in_dtype = d.in_dtype;
+    a.out_dtype = d.out_dtype;
+    a.act = d.act;
+    a.aligned = (uintptr_t)x % 16 == 0 && (uintptr_t)w % 16 == 0 && d.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0;
+    a.vec_out = (uintptr_t)y % (4 * ob) == 0 && (d.M == 1 || a.ldy % 4 == 0) &&
+                (!residual || ((uintptr_t)residual % (4 * ob) == 0 && (d.M == 1 || a.ldr % 4 == 0)));
+    return launch_linear(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PW_OK : PW_ERR_HIP;
 }
 
 pw_status pw_get_page_table(const pw_ctx* c, pw_page_entry* out) {

@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "dequant.h"
@@ -903,7 +904,7 @@ __global__ __launch_bounds__(kThreads, 3) void gate_up_own_route_kernel(FfnArgs 
     __syncthreads();   // s_cnt cleared
     if (chosen) {
         s_ids[p] = pe;
-        atomicAdd(&s_cnt[pe], 1);
+        if (ROUTE || pe >= 0) atomicAdd(&s_cnt[pe], 1);   // -1: a given route without an expert
     }
     __syncthreads();
     // the routed experts by class, then id (every wave finds the same);
@@ -912,6 +913,11 @@ __global__ __launch_bounds__(kThreads, 3) void gate_up_own_route_kernel(FfnArgs 
     const bool first = (my_bits > 4) == (a.bitplane != 0);
     const uint64_t m0 = __ballot(act && first), m1 = __ballot(act && !first);
     const int n0 = __popcll(m0), n_act = n0 + __popcll(m1);
+    if (!ROUTE && n_act == 0 && blockIdx.x == 0) {
+        // given routes without any expert: the down product finds none
+        if (tid < a.E) a.w.dg.cnt[tid] = 0;
+        if (tid < 2) a.w.dg.n_act[tid] = 0;
+    }
     if (ai >= n_act) return;
     const int arank = (act && first) ? lanes_below(m0) : n0 + lanes_below(m1);
     const int e = __ffsll((unsigned long long)__ballot(act && arank == ai)) - 1;
@@ -1047,8 +1053,12 @@ __device__ __forceinline__ float4 load_partial(const float* p) {
 // grid (ceil(d/1024), T). A token's k partial rows are consecutive in O;
 // the loads of up to 8 slots (and of two further splits of each) are issued
 // before any of them is used, and the sums keep the slot and split order.
+// GIVEN (given routes): slots without an expert have no row in O and are
+// left out, and the residual is added last, in fp32, before the one rounding
+// to y's type.
+template <class OUT, bool GIVEN>
 __global__ __launch_bounds__(kThreads) void combine_kernel(FwdWork w, int d, int k, int P, int nsplit,
-                                                           float* y) {
+                                                           const OUT* residual, OUT* y) {
     const int t = blockIdx.y;
     const int col = (blockIdx.x * kThreads + threadIdx.x) * 4;
     if (col >= d) return;
@@ -1057,9 +1067,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(FwdWork w, int d, int
         float4 o[8];
         float gj[8];
         const float* src[8];
+        bool has[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (j0 + u < k) {
+            has[u] = j0 + u < k && (!GIVEN || w.ids[t * k + j0 + u] >= 0);
+            if (has[u]) {
                 const int p = t * k + j0 + u;
                 gj[u] = w.g[p];
                 src[u] = w.O + (int64_t)p * d + col;
@@ -1074,14 +1086,14 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(FwdWork w, int d, int
             float4 qa[8], qb[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (j0 + u < k) {
+                if (has[u]) {
                     qa[u] = load_partial(src[u] + (int64_t)sp * P * d);
                     if (two) qb[u] = load_partial(src[u] + (int64_t)(sp + 1) * P * d);
                 }
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (j0 + u < k) {
+                if (has[u]) {
                     o[u].x += qa[u].x; o[u].y += qa[u].y; o[u].z += qa[u].z; o[u].w += qa[u].w;
                     if (two) {
                         o[u].x += qb[u].x; o[u].y += qb[u].y; o[u].z += qb[u].z; o[u].w += qb[u].w;
@@ -1091,7 +1103,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(FwdWork w, int d, int
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (j0 + u < k) {
+            if (has[u]) {
                 acc.x = fmaf(gj[u], o[u].x, acc.x);
                 acc.y = fmaf(gj[u], o[u].y, acc.y);
                 acc.z = fmaf(gj[u], o[u].z, acc.z);
@@ -1099,7 +1111,21 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(FwdWork w, int d, int
             }
         }
     }
-    *reinterpret_cast<float4*>(y + (int64_t)t * d + col) = acc;
+    const int64_t at = (int64_t)t * d + col;
+    if constexpr (std::is_same<OUT, float>::value) {
+        if (GIVEN && residual) {
+            const float4 r = *reinterpret_cast<const float4*>(residual + at);
+            acc.x += r.x; acc.y += r.y; acc.z += r.z; acc.w += r.w;
+        }
+        *reinterpret_cast<float4*>(y + at) = acc;
+    } else {
+        typedef __bf16 h4 __attribute__((ext_vector_type(4)));
+        if (residual) {
+            const h4 r = *reinterpret_cast<const h4*>(residual + at);
+            acc.x += (float)r[0]; acc.y += (float)r[1]; acc.z += (float)r[2]; acc.w += (float)r[3];
+        }
+        *reinterpret_cast<h4*>(y + at) = h4{(__bf16)acc.x, (__bf16)acc.y, (__bf16)acc.z, (__bf16)acc.w};
+    }
 }
 
 }  // namespace
@@ -1155,11 +1181,23 @@ hipError_t launch_down(const FfnArgs& a, const FfnPlan& p, hipStream_t s, KTimer
     return launch_ffn<1>(a, p, s, t);
 }
 
+static dim3 combine_grid(int T, int d) {
+    return dim3((unsigned)((d + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)T);
+}
+
 hipError_t launch_combine(const FwdWork& w, int T, int d, int k, int P, int nsplit, float* y,
                           hipStream_t s, KTimer t) {
-    dim3 grid((unsigned)((d + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)T);
-    return launch_timed(combine_kernel, grid, dim3(kThreads), 0, s, t.start, t.stop, w, d, k, P,
-                        nsplit, y);
+    return launch_timed(combine_kernel<float, false>, combine_grid(T, d), dim3(kThreads), 0, s, t.start, t.stop, w, d,
+                        k, P, nsplit, (const float*)nullptr, y);
+}
+
+hipError_t launch_combine_routed(const FwdWork& w, int T, int d, int k, int P, int nsplit, const void* residual,
+                                 void* y, int dtype, hipStream_t s, KTimer t) {
+    if (dtype == PW_F32)
+        return launch_timed(combine_kernel<float, true>, combine_grid(T, d), dim3(kThreads), 0, s, t.start, t.stop, w,
+                            d, k, P, nsplit, static_cast<const float*>(residual), static_cast<float*>(y));
+    return launch_timed(combine_kernel<__bf16, true>, combine_grid(T, d), dim3(kThreads), 0, s, t.start, t.stop, w, d,
+                        k, P, nsplit, static_cast<const __bf16*>(residual), static_cast<__bf16*>(y));
 }
 
 }  // namespace pw

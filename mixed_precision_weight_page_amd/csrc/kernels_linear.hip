@@ -1,0 +1,465 @@
+// Dense product with its epilogue: y = act(x w^T + b) + r, or with SwiGLU
+// y = silu(x wg^T + bg) (x wu^T + bu) + r, w holding the N gate rows and
+// then the N up rows. bf16 or fp16 operands, fp32 accumulation on the matrix
+// cores, everything after the product in fp32, one rounding to y's type.
+//
+// Up to kSkinnyTokens tokens the weights' bytes bound it: linear_skinny_kernel
+// streams them from memory straight into MFMA operands. Beyond,
+// linear_tile_kernel multiplies LDS tiles.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "pw_internal.h"
+
+namespace pw {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 x 16 x 32 product: lane (r = lane % 16, g = lane / 16) holds the 8
+// K-slots 8 g .. 8 g + 7 of row r of a and of column r of b; it gets rows
+// 4 g .. 4 g + 3 of column r of the product.
+template <class T>
+__device__ __forceinline__ f32x4 mma(const u32x4& a, const u32x4& b, const f32x4& c) {
+    if constexpr (std::is_same<T, _Float16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// ---- epilogue ----
+
+__device__ __forceinline__ float sigmoid_of(float z) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
+__device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z); }
+
+__device__ __forceinline__ float act_of(float z, int act) {
+    switch (act) {
+        case PW_ACT_RELU: return fmaxf(z, 0.0f);
+        case PW_ACT_SILU: return silu_of(z);
+        case PW_ACT_SIGMOID: return sigmoid_of(z);
+        case PW_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+        case PW_ACT_GELU_TANH:
+            // (1 + tanh u) / 2 = sigmoid(2 u)
+            return z * sigmoid_of(1.5957691216057308f * (z + 0.044715f * z * z * z));
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float load_out(const void* p, int64_t i, int dtype) {
+    if (dtype == PW_F32) return reinterpret_cast<const float*>(p)[i];
+    if (dtype == PW_BF16) return (float)reinterpret_cast<const __bf16*>(p)[i];
+    return (float)reinterpret_cast<const _Float16*>(p)[i];
+}
+__device__ __forceinline__ void store_out(void* p, int64_t i, int dtype, float v) {
+    if (dtype == PW_F32) reinterpret_cast<float*>(p)[i] = v;
+    else if (dtype == PW_BF16) reinterpret_cast<__bf16*>(p)[i] = (__bf16)v;
+    else reinterpret_cast<_Float16*>(p)[i] = (_Float16)v;
+}
+
+// One output from its sum (and the up row's sum with SwiGLU), before the
+// residual.
+template <bool GLU>
+__device__ __forceinline__ float finish(const LinearArgs& a, float z, float up, int n) {
+    if (a.bias) {
+        z += a.bias[n];
+        if (GLU) up += a.bias[a.N + n];
+    }
+    return GLU ? silu_of(z) * up : act_of(z, a.act);
+}
+
+// Four consecutive outputs n .. n + 3 of token m.
+template <bool GLU>
+__device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, const f32x4& z, const f32x4& up) {
+    if (a.vec_out && n + 3 < a.N) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = finish<GLU>(a, z[i], up[i], n + i);
+        const int64_t ro = m * a.ldr + n, yo = m * a.ldy + n;
+        if (a.out_dtype == PW_F32) {
+            if (a.residual) {
+                const f32x4 r = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.residual) + ro);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += r[i];
+            }
+            *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + yo) = f32x4{v[0], v[1], v[2], v[3]};
+        } else if (a.out_dtype == PW_BF16) {
+            typedef __bf16 h4 __attribute__((ext_vector_type(4)));
+            if (a.residual) {
+                const h4 r = *reinterpret_cast<const h4*>(reinterpret_cast<const __bf16*>(a.residual) + ro);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += (float)r[i];
+            }
+            *reinterpret_cast<h4*>(reinterpret_cast<__bf16*>(a.y) + yo) =
+                h4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        } else {
+            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+            if (a.residual) {
+                const h4 r = *reinterpret_cast<const h4*>(reinterpret_cast<const _Float16*>(a.residual) + ro);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += (float)r[i];
+            }
+            *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(a.y) + yo) =
+                h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= a.N) break;
+        float v = finish<GLU>(a, z[i], up[i], n + i);
+        if (a.residual) v += load_out(a.residual, m * a.ldr + n + i, a.out_dtype);
+        store_out(a.y, m * a.ldy + n + i, a.out_dtype, v);
+    }
+}
+
+// ---- operands ----
+
+// 8 consecutive K values from p, which need not be aligned (the loads are
+// declared with the element's alignment); left: values of the row from p on,
+// zeros past them
+struct __attribute__((packed, aligned(2))) Chunk {
+    u32x4 v;
+};
+__device__ __forceinline__ u32x4 load_chunk(const uint16_t* p, int left) {
+    if (left >= 8) return reinterpret_cast<const Chunk*>(p)->v;
+    u32x4 u = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) u[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return u;
+}
+
+// ---- few tokens ----
+
+// Workgroup: RB blocks of 16 weight rows (with SwiGLU the same RB / 2 blocks
+// of gate and of up rows), MB blocks of 16 tokens, the K range dealt to its
+// waves in pieces of 64: neighbouring waves read neighbouring 128 bytes of
+// every row, straight into MFMA operands, one piece ahead. The waves' sums
+// meet in LDS.
+template <class T, int RB, int MB, bool GLU>
+__global__ __launch_bounds__(RB * MB > 4 ? 256 : 1024) void linear_skinny_kernel(LinearArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float part[];   // [waves][RB][MB][64 lanes][4]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
+    const int n0 = blockIdx.x * kRowsOut, m0 = blockIdx.y * 16 * MB;
+    // rows past the end repeat the last one; their sums are dropped
+    const uint16_t* wp[RB];
+    const uint16_t* xp[MB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int blk = GLU ? b >> 1 : b;
+        const int64_t row = min(n0 + 16 * blk + r, a.N - 1) + (GLU && (b & 1) ? (int64_t)a.N : 0);
+        wp[b] = reinterpret_cast<const uint16_t*>(a.w) + row * a.ldw + 8 * g;
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        xp[b] = reinterpret_cast<const uint16_t*>(a.x) + (int64_t)min(m0 + 16 * b + r, a.M - 1) * a.ldx + 8 * g;
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Piece {
+        u32x4 w[RB][2], x[MB][2];
+    };
+    auto load = [&](Piece& p, int k) {
+        if (k + 64 <= a.K) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int b = 0; b < RB; ++b) p.w[b][h] = reinterpret_cast<const Chunk*>(wp[b] + k + 32 * h)->v;
+#pragma unroll
+                for (int b = 0; b < MB; ++b) p.x[b][h] = reinterpret_cast<const Chunk*>(xp[b] + k + 32 * h)->v;
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int left = a.K - (k + 32 * h + 8 * g);
+#pragma unroll
+                for (int b = 0; b < RB; ++b) p.w[b][h] = load_chunk(wp[b] + k + 32 * h, left);
+#pragma unroll
+                for (int b = 0; b < MB; ++b) p.x[b][h] = load_chunk(xp[b] + k + 32 * h, left);
+            }
+        }
+    };
+    auto multiply = [&](const Piece& p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(p.w[i][h], p.x[j][h], acc[i][j]);
+    };
+    const int step = 64 * waves;
+    Piece p0, p1;
+    int k = 64 * wave;
+    if (k < a.K) load(p0, k);
+    for (; k < a.K; k += 2 * step) {
+        if (k + step < a.K) load(p1, k + step);
+        multiply(p0);
+        if (k + 2 * step < a.K) load(p0, k + 2 * step);
+        if (k + step < a.K) multiply(p1);
+    }
+    f32x4* mine = reinterpret_cast<f32x4*>(part) + (int64_t)wave * RB * MB * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) mine[(i * MB + j) * 64] = acc[i][j];
+    __syncthreads();
+    // one (row block, token block, lane) per thread and round, the waves'
+    // sums in order
+    constexpr int kBlocks = kRowsOut / 16;
+    for (int i = threadIdx.x; i < kBlocks * MB * 64; i += blockDim.x) {
+        const int ln = i & 63, q = i >> 6, blk = q / MB, j = q - blk * MB;
+        const f32x4* src = reinterpret_cast<const f32x4*>(part) + ln;
+        f32x4 z = {0.f, 0.f, 0.f, 0.f}, up = z;
+        for (int w = 0; w < waves; ++w) {
+            if (GLU) {
+                z += src[((w * RB + 2 * blk) * MB + j) * 64];
+                up += src[((w * RB + 2 * blk + 1) * MB + j) * 64];
+            } else {
+                z += src[((w * RB + blk) * MB + j) * 64];
+            }
+        }
+        const int m = m0 + 16 * j + (ln & 15), n = n0 + 16 * blk + 4 * (ln >> 4);
+        if (m < a.M && n < a.N) put4<GLU>(a, m, n, z, up);
+    }
+}
+
+// ---- many tokens ----
+
+constexpr int BK = 64;   // K values per step: 128-byte rows in LDS
+constexpr uint32_t kOutside = 0x80000000u;   // buffer offset past every record: reads 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32) |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), (short)0, 0x7fffffff, 0x00020000);
+}
+
+// 16 bytes per lane from the buffer to LDS, lane i's to dst + 16 i (device
+// pass only: the host pass does not know the builtin)
+__device__ __forceinline__ void copy_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, uint16_t* dst, uint32_t off, int soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 16, (int)off, soff, 0, 0);
+#endif
+}
+
+// Tile: BN weight rows x BM tokens, WN x WM waves, K in steps of 64 through
+// two LDS buffers. A row's 16-byte chunk c lies at chunk position
+// c ^ (row % 8), which spreads the 16 rows of an operand read over the
+// banks. DIRECT: the rows go from memory to LDS without registers (needs
+// 16-byte aligned rows; rows and K chunks past the end read as zeros by the
+// buffer's bounds check); else through registers, with unaligned loads.
+// SwiGLU: the tile's blocks of 16 rows are gate and up rows in turn, so one
+// lane holds both sums of its outputs.
+template <class T, int BM, int BN, int WM, int WN, bool GLU, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a) {
+    constexpr int kThr = 64 * WM * WN, kWaves = WM * WN;
+    constexpr int RB = BN / WN / 16, MB = BM / WM / 16;   // blocks of a wave's tile
+    constexpr int kRows = BN + BM;                          // LDS rows: weights, then tokens
+    constexpr int kOutN = GLU ? BN / 2 : BN;
+    constexpr int QW = BN * 8 / kThr, QX = BM * 8 / kThr;   // 16-byte chunks per thread and step
+    static_assert(BN * 8 % kThr == 0 && BM * 8 % kThr == 0, "whole chunks per thread");
+    extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    // tile order: each XCD (every eighth workgroup) walks one contiguous
+    // eighth, token tiles fastest inside a band of weight tiles
+    const int tn = (a.N + kOutN - 1) / kOutN, tm = (a.M + BM - 1) / BM;
+    const int64_t used = (int64_t)tn * tm, share = (used + 7) >> 3;
+    const int64_t li = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= share || li >= used) return;
+    const int nt = (int)(li / tm), mt = (int)(li - (int64_t)nt * tm);
+    const int n0 = nt * kOutN;
+    const int64_t m0 = (int64_t)mt * BM;
+
+    // this thread's chunks: LDS row (j kWaves + wave) 8 + lane / 8, chunk
+    // position lane % 8, hence chunk (lane % 8) ^ (lane / 8) of the row
+    const int cpos = lane & 7, crow = lane >> 3, chunk = cpos ^ crow;
+    const uint16_t* wbase = reinterpret_cast<const uint16_t*>(a.w) + (int64_t)n0 * a.ldw;
+    const uint16_t* xbase = reinterpret_cast<const uint16_t*>(a.x) + m0 * a.ldx;
+    const uint16_t* ubase = wbase + (GLU ? (int64_t)a.N * a.ldw : 0);
+    const auto rw = make_rsrc(wbase), rx = make_rsrc(xbase), ru = make_rsrc(ubase);
+    uint32_t ow[QW], ox[QX];   // byte offsets of the chunks at K = 0
+#pragma unroll
+    for (int j = 0; j < QW; ++j) {
+        const int lr = (j * kWaves + wave) * 8 + crow;
+        const int row = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
+        ow[j] = n0 + row < a.N ? (uint32_t)(row * a.ldw + 8 * chunk) * 2u : kOutside;
+    }
+#pragma unroll
+    for (int j = 0; j < QX; ++j) {
+        const int row = (j * kWaves + wave) * 8 + crow;
+        ox[j] = m0 + row < a.M ? (uint32_t)(row * a.ldx + 8 * chunk) * 2u : kOutside;
+    }
+    const int S = (a.K + BK - 1) / BK;
+    u32x4 reg[DIRECT ? 1 : QW + QX];
+    // gate or up rows: LDS rows (j kWaves + wave) 8 .. + 7 lie in one block of 16
+    auto is_up = [&](int j) { return GLU && ((((j * kWaves + wave) * 8) >> 4) & 1); };
+    auto fetch = [&](int s, int buf) {
+        const int k0 = s * BK;
+        const bool in = k0 + 8 * chunk < a.K;
+        if constexpr (DIRECT) {
+            uint16_t* dst = tile_lds + buf * kRows * BK;
+#pragma unroll
+            for (int j = 0; j < QW; ++j)
+                copy_to_lds(is_up(j) ? ru : rw, dst + (j * kWaves + wave) * 8 * BK, in ? ow[j] : kOutside, k0 * 2);
+#pragma unroll
+            for (int j = 0; j < QX; ++j)
+                copy_to_lds(rx, dst + (BN + (j * kWaves + wave) * 8) * BK, in ? ox[j] : kOutside, k0 * 2);
+        } else {
+            const int left = a.K - (k0 + 8 * chunk);
+#pragma unroll
+            for (int j = 0; j < QW; ++j)
+                reg[j] = (ow[j] != kOutside && left > 0)
+                             ? load_chunk((is_up(j) ? ubase : wbase) + (ow[j] >> 1) + k0, left) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < QX; ++j)
+                reg[QW + j] = (ox[j] != kOutside && left > 0) ? load_chunk(xbase + (ox[j] >> 1) + k0, left)
+                                                              : u32x4{0u, 0u, 0u, 0u};
+        }
+    };
+    auto settle = [&](int buf) {   // registers to LDS
+        if constexpr (!DIRECT) {
+            u32x4* dst = reinterpret_cast<u32x4*>(tile_lds + buf * kRows * BK) + lane;
+#pragma unroll
+            for (int j = 0; j < QW; ++j) dst[(j * kWaves + wave) * 64] = reg[j];
+#pragma unroll
+            for (int j = 0; j < QX; ++j) dst[BN * 8 + (j * kWaves + wave) * 64] = reg[QW + j];
+        }
+    };
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int wn = wave % WN, wm = wave / WN;
+    // operand chunk of K group h: position (4 h + g) ^ (row % 8)
+    int pos[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) pos[h] = r * 8 + ((4 * h + g) ^ (r & 7));
+    auto compute = [&](int buf) {
+        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + buf * kRows * BK);
+        const u32x4* wl = base + wn * RB * 128;
+        const u32x4* xl = base + BN * 8 + wm * MB * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 fw[RB], fx[MB];
+#pragma unroll
+            for (int j = 0; j < MB; ++j) fx[j] = xl[j * 128 + pos[h]];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) fw[i] = wl[i * 128 + pos[h]];
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
+        }
+    };
+    if (S > 0) {
+        fetch(0, 0);
+        settle(0);
+    }
+    for (int s = 0; s < S; ++s) {
+        __syncthreads();   // step s is in LDS; everyone is done with the other buffer
+        if (s + 1 < S) fetch(s + 1, (s + 1) & 1);
+        compute(s & 1);
+        if (s + 1 < S) settle((s + 1) & 1);
+    }
+    // Epilogue: a wave's sums of 16 tokens at a time through its own part of
+    // the (now free) LDS, out as whole rows of its 16 RB weight rows
+    constexpr int kStride = 16 * RB + 4;   // floats; the padding spreads the tokens over the banks
+    constexpr int kQuads = (GLU ? RB / 2 : RB) * 4;   // four outputs each, per token
+    static_assert(kWaves * 16 * kStride * 4 <= 2 * kRows * BK * 2, "the sums fit the tile buffers");
+    static_assert(64 % kQuads == 0, "whole tokens per round");
+    __syncthreads();
+    float* os = reinterpret_cast<float*>(tile_lds) + wave * 16 * kStride;
+    const int q = lane % kQuads, tok = lane / kQuads;
+    const int col = GLU ? (q >> 2) * 32 + (q & 3) * 4 : q * 4;
+    const int n = n0 + wn * (GLU ? RB / 2 : RB) * 16 + q * 4;
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the former tokens are read
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4*>(os + r * kStride + 16 * i + 4 * g) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int t = tok; t < 16; t += 64 / kQuads) {
+            const int64_t m = m0 + (wm * MB + j) * 16 + t;
+            if (m >= a.M || n >= a.N) continue;
+            const f32x4 z = *reinterpret_cast<const f32x4*>(os + t * kStride + col);
+            const f32x4 up = GLU ? *reinterpret_cast<const f32x4*>(os + t * kStride + col + 16) : z;
+            put4<GLU>(a, m, n, z, up);
+        }
+    }
+}
+
+template <class T, int BM, int BN, int WM, int WN, bool GLU, bool DIRECT>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
+    constexpr int kOutN = GLU ? BN / 2 : BN;
+    const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
+    const unsigned grid = (unsigned)((tiles + 7) / 8 * 8);
+    auto kernel = linear_tile_kernel<T, BM, BN, WM, WN, GLU, DIRECT>;
+    const size_t lds = (size_t)2 * (BN + BM) * BK * 2;
+    kernel<<<grid, 64 * WM * WN, lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <class T, int RB, int MB, bool GLU>
+hipError_t launch_skinny(const LinearArgs& a, int waves, hipStream_t s) {
+    constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
+    const dim3 grid((unsigned)((a.N + kRowsOut - 1) / kRowsOut), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+    const size_t lds = (size_t)waves * RB * MB * 1024;
+    linear_skinny_kernel<T, RB, MB, GLU><<<grid, 64 * waves, lds, s>>>(a);
+    return hipGetLastError();
+}
+
+constexpr int kSkinnyTokens = 64;
+
+template <class T, bool GLU>
+hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
+    if (a.M <= kSkinnyTokens) {
+        const int mb = (a.M + 15) / 16;
+        const int64_t rows = GLU ? 2ll * a.N : a.N;
+        int waves = 4;
+        const int64_t blocks = (rows + 31) / 32 * (rows <= 8192 ? mb : 1);
+        while (waves < 16 && blocks * waves < 4096 && waves * 64 < a.K) waves *= 2;
+        if (mb == 1 || rows <= 8192) return launch_skinny<T, 2, 1, GLU>(a, waves, s);
+        waves = std::min(waves, 4);
+        if (mb == 2) return launch_skinny<T, 4, 2, GLU>(a, waves, s);
+        return launch_skinny<T, 4, 4, GLU>(a, waves, s);
+    }
+    if (!a.aligned) return launch_tile<T, 64, 64, 2, 2, GLU, false>(a, s);
+    const int64_t big = (int64_t)((a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256)) * ((a.M + 255) / 256);
+    if (big >= 128) return launch_tile<T, 256, 256, 4, 2, GLU, true>(a, s);
+    const int64_t mid = (int64_t)((a.N + (GLU ? 63 : 127)) / (GLU ? 64 : 128)) * ((a.M + 127) / 128);
+    if (mid >= 128) return launch_tile<T, 128, 128, 2, 2, GLU, true>(a, s);
+    return launch_tile<T, 64, 64, 2, 2, GLU, true>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
+    const bool glu = a.act == PW_ACT_SWIGLU;
+    if (a.in_dtype == PW_BF16) return glu ? launch_linear_t<__bf16, true>(a, s) : launch_linear_t<__bf16, false>(a, s);
+    return glu ? launch_linear_t<_Float16, true>(a, s) : launch_linear_t<_Float16, false>(a, s);
+}
+
+}  // namespace pw

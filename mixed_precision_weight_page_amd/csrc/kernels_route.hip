@@ -342,7 +342,7 @@ __device__ __forceinline__ void finalize(int T, int E, int k, const FwdWork& w, 
     const int P = T * k;
     for (int p = threadIdx.x; p < P; p += kBlock) {
         const int e = id_of(p);
-        w.sorted[s_off[e] + rank_of(p)] = p;
+        if (e >= 0) w.sorted[s_off[e] + rank_of(p)] = p;   // -1: a given route without an expert
     }
 }
 
@@ -480,6 +480,46 @@ __global__ __launch_bounds__(128) void route_decode_kernel(RouteArgs a, FwdWork 
     else route_row(a, w, t, threadIdx.x < 16, nullptr, a.group != 0);
 }
 
+// ---- given routes ----
+// grid T, 128 threads: wave 0 takes token t's k ids and weights (lane j slot
+// j), wave 1 its activation statistics, as in route_decode_kernel.
+__global__ __launch_bounds__(128) void accept_routes_kernel(RouteArgs a, FwdWork w, const int32_t* ids, const float* g) {
+    const int t = blockIdx.x;
+    if (threadIdx.x >= 64) {
+        if (a.x) {
+            const XStat st = lanes_stat<64>(a.x + (int64_t)t * a.d, a.d);
+            if (threadIdx.x == 64) w.xst[t] = st;
+        }
+        return;
+    }
+    const int j = threadIdx.x;
+    const int p = t * a.k + j;
+    int e = -1;
+    float wt = 0.0f;
+    if (j < a.k) {
+        e = ids[p];
+        wt = g[p];
+        if ((uint32_t)e >= (uint32_t)a.E) e = -1;
+    }
+    // an expert's pair list has room for one pair per token: a second slot
+    // with the same expert adds its weight to the first (y is linear in it)
+    const int mine = e;
+    float sum = wt;
+    for (int i = 0; i < a.k; ++i) {
+        const int oe = __shfl(mine, i);
+        const float ow = __shfl(wt, i);
+        if (mine >= 0 && oe == mine) {
+            if (i < j) e = -1;
+            else if (i > j) sum += ow;
+        }
+    }
+    if (j < a.k) {
+        w.ids[p] = e;
+        w.g[p] = sum;
+        if (a.group && e >= 0) group_pair(w.dg, w.tcap, a.bits, e, p);
+    }
+}
+
 // grid (E, C), 256 threads: rank of expert e's pairs in token order among
 // the tokens of chunk c, and their count.
 __global__ __launch_bounds__(256) void rank_kernel(int T, int k, int C, FwdWork w) {
@@ -531,6 +571,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(int P, int k, int C, FwdWo
     const int p = blockIdx.x * 256 + threadIdx.x;
     if (p >= P) return;
     const int e = w.ids[p];
+    if (e < 0) return;   // a given route without an expert
     const int c = (p / k) / kRankChunk;
     w.sorted[w.off[e] + w.cpre[e * C + c] + w.rank[p]] = p;
 }
@@ -552,6 +593,31 @@ hipError_t launch_route_decode(const RouteArgs& a, const FwdWork& w, hipStream_t
     return launch_timed(route_decode_kernel, dim3((unsigned)a.T), dim3(128), 0, s, t.start, t.stop, a, w);
 }
 
+hipError_t launch_accept_routes(const RouteArgs& a, const FwdWork& w, const int32_t* ids, const float* g, hipStream_t s,
+                                KTimer t) {
+    return launch_timed(accept_routes_kernel, dim3((unsigned)a.T), dim3(128), 0, s, t.start, t.stop, a, w, ids, g);
+}
+
+// Sorted pairs, offsets and token tiles of routed pairs.
+static hipError_t launch_group(const RouteArgs& a, const FwdWork& w, const DevTable& tab, hipStream_t s,
+                               hipEvent_t stop) {
+    const hipEvent_t none = nullptr;
+    if (a.T * a.k <= kFusedMaxPairs)
+        return launch_timed(group_small_kernel, dim3(1), dim3(kBlock), 0, s, none, stop, a.T, a.E, a.k,
+                            a.tiles, w, tab);
+    const int C = (a.T + kRankChunk - 1) / kRankChunk;
+    hipError_t err = launch_timed(rank_kernel, dim3(a.E, C), dim3(256), 0, s, none, none, a.T, a.k, C, w);
+    if (err != hipSuccess) return err;
+    err = launch_timed(offsets_kernel, dim3(1), dim3(kBlock), 0, s, none, none, a.E, C, a.tiles, w, tab);
+    if (err != hipSuccess) return err;
+    const int P = a.T * a.k;
+    return launch_timed(scatter_kernel, dim3((P + 255) / 256), dim3(256), 0, s, none, stop, P, a.k, C, w);
+}
+
+hipError_t launch_group_pairs(const RouteArgs& a, const FwdWork& w, const DevTable& tab, hipStream_t s) {
+    return launch_group(a, w, tab, s, nullptr);
+}
+
 hipError_t launch_route(const RouteArgs& a, const FwdWork& w, const DevTable& tab, hipStream_t s,
                         KTimer t) {
     const hipEvent_t none = nullptr;
@@ -561,16 +627,7 @@ hipError_t launch_route(const RouteArgs& a, const FwdWork& w, const DevTable& ta
     hipError_t err = launch_timed(route_kernel, dim3((a.T + per_block - 1) / per_block), dim3(256), 0, s, t.start,
                                   none, a, w);
     if (err != hipSuccess) return err;
-    if (a.T * a.k <= kFusedMaxPairs)
-        return launch_timed(group_small_kernel, dim3(1), dim3(kBlock), 0, s, none, t.stop, a.T, a.E, a.k,
-                            a.tiles, w, tab);
-    const int C = (a.T + kRankChunk - 1) / kRankChunk;
-    err = launch_timed(rank_kernel, dim3(a.E, C), dim3(256), 0, s, none, none, a.T, a.k, C, w);
-    if (err != hipSuccess) return err;
-    err = launch_timed(offsets_kernel, dim3(1), dim3(kBlock), 0, s, none, none, a.E, C, a.tiles, w, tab);
-    if (err != hipSuccess) return err;
-    const int P = a.T * a.k;
-    return launch_timed(scatter_kernel, dim3((P + 255) / 256), dim3(256), 0, s, none, t.stop, P, a.k, C, w);
+    return launch_group(a, w, tab, s, t.stop);
 }
 
 }  // namespace pw

@@ -105,6 +105,8 @@ struct Layout {
     uint64_t partial, stats_end;
     uint64_t dg, dg_bytes;   // the two counter sets of the streaming kernels' grouping (outside the
                              // bytes the statistics pass reuses; zeroed when the workspace is bound)
+    uint64_t rg;             // two more of the same size for forwards of given routes, which clear
+                             // what they count in at each call (so that a captured one can be replayed)
     uint64_t total;
 };
 
@@ -161,6 +163,15 @@ hipError_t launch_route(const RouteArgs& a, const FwdWork& w, const DevTable& ta
 // Router of the streaming kernels: top-k, weights, token statistics and the
 // grouping of FwdWork::dg, in one launch over many workgroups.
 hipError_t launch_route_decode(const RouteArgs& a, const FwdWork& w, hipStream_t s, KTimer t = {});
+// Given routes into the forward's scratch: ids outside [0, E) become -1, an
+// expert named twice by a token keeps its first slot with the summed weight.
+// RouteArgs as for launch_route_decode (logits unused; group: also group the
+// pairs for the streaming kernels).
+hipError_t launch_accept_routes(const RouteArgs& a, const FwdWork& w, const int32_t* ids, const float* g, hipStream_t s,
+                                KTimer t = {});
+// The matrix-core kernels' sorted pairs, offsets and token tiles from the
+// scratch's ids (-1: no expert).
+hipError_t launch_group_pairs(const RouteArgs& a, const FwdWork& w, const DevTable& tab, hipStream_t s);
 // n int32 zeros at p (one small kernel)
 hipError_t launch_zero_i32(int32_t* p, uint64_t n, hipStream_t s);
 
@@ -203,6 +214,44 @@ hipError_t launch_gate_up(const FfnArgs& a, const FfnPlan& p, hipStream_t s, KTi
 hipError_t launch_down(const FfnArgs& a, const FfnPlan& p, hipStream_t s, KTimer t = {});
 hipError_t launch_combine(const FwdWork& w, int T, int d, int k, int P, int nsplit, float* y,
                           hipStream_t s, KTimer t = {});
+// The same for given routes: pairs without an expert are left out, residual
+// (NULL: none) and y are fp32 or bf16 (dtype, a pw_dtype).
+hipError_t launch_combine_routed(const FwdWork& w, int T, int d, int k, int P, int nsplit, const void* residual,
+                                 void* y, int dtype, hipStream_t s, KTimer t = {});
+
+// Gated router (kernels_gate.hip)
+struct GateArgs {
+    const void* logits;     // [T, E] of dtype, rows ld elements apart
+    int64_t ld;
+    int dtype;              // pw_dtype
+    const float* bias;      // [E] or NULL
+    const uint8_t* mask;    // [T] or NULL
+    int T, E, k;
+    int score, n_group, topk_group, group_top2, renorm;
+    float scale;
+    int32_t* ids;           // [T, k]
+    float* g;               // [T, k]
+    int32_t* counts;        // [E] or NULL
+    // set by the launcher: lanes that scan one group, and e / (E / n_group)
+    // as (e group_magic) >> 20
+    int group_lanes;
+    uint32_t group_magic;
+};
+hipError_t launch_gate(const GateArgs& a, hipStream_t s);
+
+// Dense product (kernels_linear.hip)
+struct LinearArgs {
+    const void *x, *w;
+    const float* bias;
+    const void* residual;
+    void* y;
+    int64_t ldx, ldw, ldr, ldy;   // elements between rows
+    int M, N, K;
+    int in_dtype, out_dtype, act;
+    int aligned;    // 16-byte aligned rows of x and w
+    int vec_out;    // rows of y (and residual) aligned to four elements
+};
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
 struct GemmArgs {
     const uint8_t* pool;

@@ -62,6 +62,24 @@ class BudgetPolicy(ctypes.Structure):
 
 BUDGET_KEEP, BUDGET_SHRINK, BUDGET_GROW, BUDGET_INIT = 0, 1, 2, 3
 
+class GateDesc(ctypes.Structure):
+    """pw_gate_desc: score, groups, groups kept, group score, renormalisation, scale."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top2", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class LinearDesc(ctypes.Structure):
+    """pw_linear_desc: sizes, types, activation, row distances in elements."""
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # pw_dtype
+SCORES = {"softmax": 0, "sigmoid": 1}                                 # pw_score
+GROUP_SCORES = {"max": 0, "top2": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "sigmoid": 3, "gelu": 4, "gelu_tanh": 5, "swiglu": 6}   # pw_act
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "pw_create": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.POINTER(_P)]),
@@ -76,6 +94,10 @@ _SIGNATURES = {
     "pw_moe_forward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P]),
     "pw_moe_forward_noalloc": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P]),
     "pw_route": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P, _P]),
+    "pw_route_gated": (ctypes.c_int, [_P, ctypes.POINTER(GateDesc), _P, ctypes.c_int32, ctypes.c_int64, _P, _P,
+                                      ctypes.c_int32, _P, _P, _P, _P]),
+    "pw_moe_forward_routed": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, _P, _P, ctypes.c_int32, _P]),
+    "pw_linear": (ctypes.c_int, [ctypes.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P]),
     "pw_get_page_table": (ctypes.c_int, [_P, ctypes.POINTER(PageEntry)]),
     "pw_get_loss_table": (ctypes.c_int, [_P, _P, _P]),
     "pw_solve_allocation": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, ctypes.c_uint64, _P]),
@@ -136,6 +158,86 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _here(name: str, *tensors):
+    """The calls below launch on the current device: every tensor lives there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _rows(t: torch.Tensor, dtypes, shape, name: str):
+    """Pointer and row distance (in elements) of a 2-d device tensor whose
+    rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _other_stream(stream):
+    """None if `stream` is the current one (or None), else it as a torch stream."""
+    if stream is None:
+        return None
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    return None if s.cuda_stream == torch.cuda.current_stream().cuda_stream else s
+
+
+def _call_on(stream, tensors, call):
+    """call() with `stream` as the current one: what it allocates belongs to
+    that stream, and what it reads or writes is not reused before the stream
+    is done with it."""
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+           out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """pw_linear: y = act(x w^T + bias) + residual. x [M, K] and w [N, K] (with
+    act "swiglu" [2 N, K]: gate rows, then up rows) bf16 or fp16, bias fp32,
+    residual and y [M, N] of out_dtype (default: y's, residual's or x's
+    type); rows may be strided. act: none, relu, silu, sigmoid, gelu,
+    gelu_tanh, swiglu. residual may be y."""
+    side = _other_stream(stream)
+    if side is not None:
+        return _call_on(side, (x, w, bias, residual, y), lambda: linear(x, w, bias, act, residual, y, out_dtype))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be 2-d tensors")
+    (M, K), rows = x.shape, w.shape[0]
+    if act == "swiglu" and rows % 2:
+        raise ValueError("swiglu: w must have as many gate as up rows")
+    N = rows // 2 if act == "swiglu" else rows
+    xp, ldx = _rows(x, (torch.bfloat16, torch.float16), (M, K), "x")
+    wp, ldw = _rows(w, (x.dtype,), (rows, K), "w")
+    if out_dtype is None:
+        out_dtype = y.dtype if y is not None else (residual.dtype if residual is not None else x.dtype)
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+    if bias is not None and tuple(bias.shape) != (rows,):
+        raise ValueError(f"bias must be [{rows}]")
+    bp = None if bias is None else _dev(bias, torch.float32, "bias")
+    rp, ldr = (None, N) if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    yp, ldy = _rows(y, (out_dtype,), (M, N), "y")
+    _here("linear", x, w, bias, residual, y)
+    desc = LinearDesc(M, N, K, _DTYPES[x.dtype], _DTYPES[out_dtype], ACTIVATIONS[act], ldx, ldw, ldr, ldy)
+    _check(lib().pw_linear(ctypes.byref(desc), xp, wp, bp, rp, yp, _stream()))
+    return y
 
 
 def _host_array(a, dtype, n: int, name: str) -> np.ndarray:
@@ -374,6 +476,93 @@ class PagedMoELayer:
                               ids.data_ptr(), g.data_ptr(), counts.data_ptr(), _stream(stream)),
                self._ctx)
         return ids, g, counts
+
+    def route_gated(self, logits: torch.Tensor, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                    n_group: int = 1, topk_group: int = 1, group_score: str = "max", renorm: bool = False,
+                    scale: float = 1.0, mask: Optional[torch.Tensor] = None, with_counts: bool = True, stream=None):
+        """pw_route_gated: (ids int32 [T, k], weights fp32 [T, k], pairs per
+        expert int32 [E] or None). logits [T, E] fp32, bf16 or fp16 (rows may
+        be strided); score "softmax" or "sigmoid"; bias fp32 [E] counts in
+        the choice only; group_score "max" or "top2"; mask bool or uint8 [T],
+        0 for padded tokens."""
+        side = _other_stream(stream)
+        if side is not None:
+            return _call_on(side, (logits, bias, mask), lambda: self.route_gated(
+                logits, score, bias, n_group, topk_group, group_score, renorm, scale, mask, with_counts))
+        if score not in SCORES or group_score not in GROUP_SCORES:
+            raise ValueError("score must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
+        if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+            raise ValueError("logits must be [T, E]")
+        T = logits.shape[0]
+        lp, ld = _rows(logits, _DTYPES, (T, self.E), "logits")
+        if bias is not None and tuple(bias.shape) != (self.E,):
+            raise ValueError(f"bias must be [{self.E}]")
+        bp = None if bias is None else _dev(bias, torch.float32, "bias")
+        mp = None
+        if mask is not None:
+            if tuple(mask.shape) != (T,) or mask.dtype not in (torch.bool, torch.uint8):
+                raise ValueError(f"mask must be bool or uint8 [{T}]")
+            mp = _dev(mask, mask.dtype, "mask")
+        _here("route_gated", logits, bias, mask)
+        ids = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
+        g = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
+        counts = torch.empty((self.E,), dtype=torch.int32, device=logits.device) if with_counts else None
+        desc = GateDesc(SCORES[score], n_group, topk_group, GROUP_SCORES[group_score], int(bool(renorm)), scale)
+        _check(lib().pw_route_gated(self._ctx, ctypes.byref(desc), lp, _DTYPES[logits.dtype], ld, bp, mp, T,
+                                    ids.data_ptr(), g.data_ptr(), None if counts is None else counts.data_ptr(),
+                                    _stream()), self._ctx)
+        return ids, g, counts
+
+    def moe_forward_routed(self, x: torch.Tensor, ids: torch.Tensor, g: torch.Tensor,
+                           residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                           out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+        """pw_moe_forward_routed: the experts' products for given ids int32
+        [T, k] (-1: no expert) and weights fp32 [T, k], added to residual
+        [T, d] if given. y and residual are float32 or bfloat16 (out_dtype;
+        default: y's or residual's type, else float32); residual may be y."""
+        side = _other_stream(stream)
+        if side is not None:
+            return _call_on(side, (x, ids, g, residual, y),
+                            lambda: self.moe_forward_routed(x, ids, g, residual, y, out_dtype))
+        T = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != self.d or tuple(ids.shape) != (T, self.k) or tuple(g.shape) != (T, self.k):
+            raise ValueError("x must be [T, d], ids and g [T, k]")
+        if out_dtype is None:
+            out_dtype = y.dtype if y is not None else (residual.dtype if residual is not None else torch.float32)
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        for t, n in ((residual, "residual"), (y, "y")):
+            if t is not None and tuple(t.shape) != (T, self.d):
+                raise ValueError(f"{n} must be [T, d]")
+        if y is None:
+            y = torch.empty((T, self.d), dtype=out_dtype, device=x.device)
+        _here("moe_forward_routed", x, ids, g, residual, y)
+        _check(lib().pw_moe_forward_routed(self._ctx, _dev(x, torch.bfloat16, "x"), _dev(ids, torch.int32, "ids"),
+                                           _dev(g, torch.float32, "g"), T,
+                                           None if residual is None else _dev(residual, out_dtype, "residual"),
+                                           _dev(y, out_dtype, "y"), _DTYPES[out_dtype], _stream()), self._ctx)
+        return y
+
+    def moe_block(self, x: torch.Tensor, gate_w: torch.Tensor, gate_logit_bias: Optional[torch.Tensor] = None,
+                  shared: Optional[Sequence[torch.Tensor]] = None, residual: Optional[torch.Tensor] = None,
+                  y: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16, stream=None, **gate):
+        """A whole mixture-of-experts block on x bf16 [T, d]: router logits
+        (linear with gate_w [E, d], in fp32), route_gated with the arguments
+        in `gate`, the shared expert if given (w_gate_up [2 F, d] and w_down
+        [d, F], any F) and the routed experts, all added to residual. Returns
+        (y, ids, weights, pairs per expert)."""
+        side = _other_stream(stream)
+        if side is not None:
+            tensors = (x, gate_w, gate_logit_bias, residual, y, gate.get("bias"), gate.get("mask"), *(shared or ()))
+            return _call_on(side, tensors, lambda: self.moe_block(x, gate_w, gate_logit_bias, shared, residual, y,
+                                                                  out_dtype, **gate))
+        logits = linear(x, gate_w, gate_logit_bias, out_dtype=torch.float32)
+        ids, g, counts = self.route_gated(logits, **gate)
+        base = residual
+        if shared is not None:
+            w_gate_up, w_down = shared
+            base = linear(linear(x, w_gate_up, act="swiglu"), w_down, residual=residual, out_dtype=out_dtype)
+        return self.moe_forward_routed(x, ids, g, base, y, out_dtype), ids, g, counts
 
     # ---- inspection ----
     def get_page_table(self):
