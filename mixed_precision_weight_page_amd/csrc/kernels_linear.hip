@@ -43,19 +43,6 @@ __device__ __forceinline__ float sigmoid_of(float z) {
 
 __device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z); }
 
-__device__ __forceinline__ float act_of(float z, int act) {
-    switch (act) {
-        case PW_ACT_RELU: return fmaxf(z, 0.0f);
-        case PW_ACT_SILU: return silu_of(z);
-        case PW_ACT_SIGMOID: return sigmoid_of(z);
-        case PW_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-        case PW_ACT_GELU_TANH:
-            // (1 + tanh u) / 2 = sigmoid(2 u)
-            return z * sigmoid_of(1.5957691216057308f * (z + 0.044715f * z * z * z));
-        default: return z;
-    }
-}
-
 __device__ __forceinline__ float load_out(const void* p, int64_t i, int dtype) {
     if (dtype == PW_F32) return reinterpret_cast<const float*>(p)[i];
     if (dtype == PW_BF16) return (float)reinterpret_cast<const __bf16*>(p)[i];
@@ -67,59 +54,89 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, int dtype, float v
     else reinterpret_cast<_Float16*>(p)[i] = (_Float16)v;
 }
 
-// One output from its sum (and the up row's sum with SwiGLU), before the
-// residual.
-template <bool GLU>
-__device__ __forceinline__ float finish(const LinearArgs& a, float z, float up, int n) {
-    if (a.bias) {
-        z += a.bias[n];
-        if (GLU) up += a.bias[a.N + n];
+// Four consecutive values: residual bits, their addition, the store.
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 load_quad(const void* p, int64_t i, int dtype) {
+    if (dtype == PW_F32) return *reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    return u32x4{u.x, u.y, 0u, 0u};
+}
+__device__ __forceinline__ void add_quad(float (&v)[4], const u32x4& r, int dtype) {
+    if (dtype == PW_F32) {
+        const f32x4 f = __builtin_bit_cast(f32x4, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += f[e];
+    } else if (dtype == PW_BF16) {
+        const bf16x4 f = __builtin_bit_cast(bf16x4, uint2{r[0], r[1]});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += (float)f[e];
+    } else {
+        const f16x4 f = __builtin_bit_cast(f16x4, uint2{r[0], r[1]});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += (float)f[e];
     }
-    return GLU ? silu_of(z) * up : act_of(z, a.act);
+}
+__device__ __forceinline__ void store_quad(void* p, int64_t i, int dtype, const float (&v)[4]) {
+    if (dtype == PW_F32)
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+    else if (dtype == PW_BF16)
+        *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p) + i) =
+            bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    else
+        *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(p) + i) =
+            f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
 }
 
-// Four consecutive outputs n .. n + 3 of token m.
+// The activation of n quads (one branch for all of them).
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N][4], int act) {
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[t][e] = f(v[t][e]);
+    };
+    switch (act) {
+        case PW_ACT_RELU: each([](float z) { return z > 0.0f || z != z ? z : 0.0f; }); break;
+        case PW_ACT_SILU: each([](float z) { return silu_of(z); }); break;
+        case PW_ACT_SIGMOID: each([](float z) { return sigmoid_of(z); }); break;
+        case PW_ACT_GELU: each([](float z) { return 0.5f * z * erfcf(-0.70710678118654752f * z); }); break;
+        case PW_ACT_GELU_TANH:
+            // (1 + tanh u) / 2 = sigmoid(2 u)
+            each([](float z) { return z * sigmoid_of(1.5957691216057308f * (z + 0.044715f * z * z * z)); });
+            break;
+        default: break;
+    }
+}
+
+// Outputs n .. n + 3 of token m from their sums.
 template <bool GLU>
-__device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, const f32x4& z, const f32x4& up) {
-    if (a.vec_out && n + 3 < a.N) {
-        float v[4];
+__device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, f32x4 z, f32x4 up) {
+    const bool vec = a.vec_out && n + 3 < a.N;
+    u32x4 res = {0u, 0u, 0u, 0u};
+    if (a.residual && vec) res = load_quad(a.residual, m * a.ldr + n, a.out_dtype);
+    float v[1][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = finish<GLU>(a, z[i], up[i], n + i);
-        const int64_t ro = m * a.ldr + n, yo = m * a.ldy + n;
-        if (a.out_dtype == PW_F32) {
-            if (a.residual) {
-                const f32x4 r = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.residual) + ro);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += r[i];
-            }
-            *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + yo) = f32x4{v[0], v[1], v[2], v[3]};
-        } else if (a.out_dtype == PW_BF16) {
-            typedef __bf16 h4 __attribute__((ext_vector_type(4)));
-            if (a.residual) {
-                const h4 r = *reinterpret_cast<const h4*>(reinterpret_cast<const __bf16*>(a.residual) + ro);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += (float)r[i];
-            }
-            *reinterpret_cast<h4*>(reinterpret_cast<__bf16*>(a.y) + yo) =
-                h4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        } else {
-            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-            if (a.residual) {
-                const h4 r = *reinterpret_cast<const h4*>(reinterpret_cast<const _Float16*>(a.residual) + ro);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += (float)r[i];
-            }
-            *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(a.y) + yo) =
-                h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    for (int e = 0; e < 4; ++e) {
+        if (a.bias && n + e < a.N) {
+            z[e] += a.bias[n + e];
+            if (GLU) up[e] += a.bias[a.N + n + e];
         }
+        v[0][e] = GLU ? silu_of(z[e]) * up[e] : z[e];
+    }
+    if constexpr (!GLU) act_all(v, a.act);
+    if (vec) {
+        if (a.residual) add_quad(v[0], res, a.out_dtype);
+        store_quad(a.y, m * a.ldy + n, a.out_dtype, v[0]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= a.N) break;
-        float v = finish<GLU>(a, z[i], up[i], n + i);
-        if (a.residual) v += load_out(a.residual, m * a.ldr + n + i, a.out_dtype);
-        store_out(a.y, m * a.ldy + n + i, a.out_dtype, v);
+    for (int e = 0; e < 4; ++e) {
+        if (n + e >= a.N) break;
+        float o = v[0][e];
+        if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, a.out_dtype);
+        store_out(a.y, m * a.ldy + n + e, a.out_dtype, o);
     }
 }
 
@@ -259,6 +276,209 @@ __device__ __forceinline__ void copy_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, 
 #endif
 }
 
+// byte offset of K value k0, 0 past the end (the lanes are out of bounds there)
+__device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 : 0; }
+
+// Epilogue of a wave's tile: the sums of 16 tokens at a time through the
+// wave's own part of the (free) LDS, out as whole rows of its 16 RB weight
+// rows. n0, m0: the wave's first output column and token.
+template <int RB>
+__host__ __device__ constexpr int out_stage_floats() { return 16 * (16 * RB + 4); }   // the padding spreads the tokens over the banks
+
+template <int RB, int MB, bool GLU>
+__device__ __forceinline__ void put_tile(const LinearArgs& a, const f32x4 (&acc)[RB][MB], float* os, int n0, int64_t m0) {
+    constexpr int kStride = 16 * RB + 4;
+    constexpr int kQuads = (GLU ? RB / 2 : RB) * 4;   // four outputs each, per token
+    constexpr int kStep = 64 / kQuads, kIter = 16 / kStep;
+    static_assert(64 % kQuads == 0 && 16 % kStep == 0, "whole tokens per round");
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int q = lane % kQuads, tok = lane / kQuads;
+    const int col = GLU ? (q >> 2) * 32 + (q & 3) * 4 : q * 4;
+    const int n = n0 + q * 4;
+    // the lane's four columns are the same for every token
+    const bool vec = a.vec_out && n + 3 < a.N;
+    f32x4 bz = {0.f, 0.f, 0.f, 0.f}, bu = bz;
+    if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (n + e < a.N) {
+                bz[e] = a.bias[n + e];
+                if (GLU) bu[e] = a.bias[a.N + n + e];
+            }
+        }
+    }
+    // one round of the loop serves 16 tokens: the code of the activations is
+    // there once, and all of a round's residual loads are in flight before
+    // the sums are staged
+#pragma unroll 1
+    for (int j = 0; j < MB; ++j) {
+        const int64_t mj = m0 + j * 16 + tok;
+        float v[kIter][4];
+        u32x4 res[kIter];
+        if (a.residual && vec) {
+#pragma unroll
+            for (int t = 0; t < kIter; ++t)
+                if (mj + t * kStep < a.M) res[t] = load_quad(a.residual, (mj + t * kStep) * a.ldr + n, a.out_dtype);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the former tokens are read
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int J = 0; J < MB; ++J) {
+            if (J != j) continue;
+#pragma unroll
+            for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4*>(os + r * kStride + 16 * i + 4 * g) = acc[i][J];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int t = 0; t < kIter; ++t) {
+            const float* row = os + (tok + t * kStep) * kStride + col;
+            const f32x4 z = *reinterpret_cast<const f32x4*>(row) + bz;
+            if constexpr (GLU) {
+                const f32x4 up = *reinterpret_cast<const f32x4*>(row + 16) + bu;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[t][e] = silu_of(z[e]) * up[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[t][e] = z[e];
+            }
+        }
+        if constexpr (!GLU) act_all(v, a.act);
+#pragma unroll
+        for (int t = 0; t < kIter; ++t) {
+            const int64_t m = mj + t * kStep;
+            if (m >= a.M || n >= a.N) continue;
+            if (vec) {
+                if (a.residual) add_quad(v[t], res[t], a.out_dtype);
+                store_quad(a.y, m * a.ldy + n, a.out_dtype, v[t]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (n + e >= a.N) break;
+                    float o = v[t][e];
+                    if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, a.out_dtype);
+                    store_out(a.y, m * a.ldy + n + e, a.out_dtype, o);
+                }
+            }
+        }
+    }
+}
+
+// Tile of this workgroup, or false past the last. Each XCD (every eighth
+// workgroup) walks one contiguous eighth of the tiles, in bands of kBand
+// token tiles with the band's token tiles fastest: the 32 workgroups that
+// run together on an XCD share 8 token and 4 weight tiles through its L2.
+constexpr int kBand = 8;
+__device__ __forceinline__ bool tile_of(int tn, int tm, int& nt, int& mt) {
+    const int64_t used = (int64_t)tn * tm, share = (used + 7) >> 3;
+    const int64_t at = blockIdx.x >> 3, li = (int64_t)(blockIdx.x & 7) * share + at;
+    if (at >= share || li >= used) return false;
+    const int band = (int)(li / ((int64_t)kBand * tn));
+    const int in = (int)(li - (int64_t)band * kBand * tn);
+    const int wide = min(kBand, tm - band * kBand);
+    nt = in / wide;
+    mt = band * kBand + in - nt * wide;
+    return true;
+}
+
+// Large products: 256 weight rows x 256 tokens, 8 waves of 128 x 64 each, K
+// in stages of 32 (64-byte LDS rows) through four LDS slots.
+//
+// The two waves of a SIMD take turns: a stage is a phase of operand reads
+// (12 of 16 bytes a lane, and the copies of the stage after the next two
+// into their slot) and a phase of 32 matrix instructions; waves 4 .. 7 run
+// one phase behind waves 0 .. 3, so that one wave of each SIMD multiplies
+// while the other reads. Phases end at barriers. With stage s read in phases
+// 2 s and 2 s + 1, its slot is free from phase 2 s + 2 on, when the first
+// waves copy stage s + 4 into it; those copies have to be whole before phase
+// 2 s + 8, and every wave waits for its own at the end of its read phase of
+// stage s + 3, two later stages still on their way (8 copies a thread).
+// Copies past the last stage read zeros (out of the buffer's bounds) and
+// keep the counts alike.
+//
+// A row's 16-byte chunk c lies at position c ^ (row / 4 % 4): the 16 rows
+// of an operand read fall on different banks.
+constexpr int kPhRows = 512, kPhSlots = 4;
+template <class T, bool GLU>
+__global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
+    constexpr int RB = 8, MB = 4, kK = 32;
+    constexpr int kOutN = GLU ? 128 : 256;
+    extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    int nt, mt;
+    if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + 255) / 256, nt, mt)) return;
+    const int n0 = nt * kOutN;
+    const int64_t m0 = (int64_t)mt * 256;
+    // copies: 4 a thread and stage, each instruction of a wave 16 rows; rows
+    // 128 j' + 16 wave + lane / 4 of the weights (j = 0, 1) and tokens
+    const int crow = lane >> 2, chunk = (lane & 3) ^ ((crow >> 2) & 3);
+    const uint16_t* wbase = reinterpret_cast<const uint16_t*>(a.w) + (int64_t)n0 * a.ldw;
+    const uint16_t* xbase = reinterpret_cast<const uint16_t*>(a.x) + m0 * a.ldx;
+    // SwiGLU: the tile's blocks of 16 rows are gate and up rows in turn (a
+    // wave's copies are always one kind: 16 wave and 128 + 16 wave)
+    const bool up = GLU && (wave & 1);
+    const auto rw = make_rsrc(wbase + (up ? (int64_t)a.N * a.ldw : 0)), rx = make_rsrc(xbase);
+    uint32_t off[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int lr = 128 * j + 16 * wave + crow;
+        const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
+        off[j] = n0 + wr < a.N ? (uint32_t)(wr * a.ldw + 8 * chunk) * 2u : kOutside;
+        off[2 + j] = m0 + lr < a.M ? (uint32_t)(lr * a.ldx + 8 * chunk) * 2u : kOutside;
+    }
+    auto copy = [&](int s) {
+        const int k0 = s * kK;
+        const bool in = k0 + 8 * chunk < a.K;
+        uint16_t* dst = tile_lds + (s & (kPhSlots - 1)) * kPhRows * kK;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            copy_to_lds(j < 2 ? rw : rx, dst + (128 * j + 16 * wave) * kK, in ? off[j] : kOutside, in_bytes(k0, a.K));
+    };
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int wn = wave & 1, wm = wave >> 1;
+    const int pos = r * 4 + (g ^ ((r >> 2) & 3));
+    const int S = (a.K + kK - 1) / kK;
+    copy(0);
+    copy(1);
+    copy(2);
+    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+    if (wave >= 4) asm volatile("s_barrier" ::: "memory");
+    for (int s = 0; s < S; ++s) {
+        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + (s & (kPhSlots - 1)) * kPhRows * kK) + pos;
+        u32x4 fw[RB], fx[MB];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) fx[j] = base[(256 + (wm * MB + j) * 16) * 4];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) fw[i] = base[(wn * RB + i) * 64];
+        copy(s + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // the copies past the last stage land before the LDS is used again
+    if (wave < 4) asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    static_assert(8 * out_stage_floats<RB>() * 4 <= kPhSlots * kPhRows * kK * 2, "the sums fit the slots");
+    put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
+                          n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
+}
+
 // Tile: BN weight rows x BM tokens, WN x WM waves, K in steps of 64 through
 // two LDS buffers. A row's 16-byte chunk c lies at chunk position
 // c ^ (row % 8), which spreads the 16 rows of an operand read over the
@@ -279,13 +499,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
-    // tile order: each XCD (every eighth workgroup) walks one contiguous
-    // eighth, token tiles fastest inside a band of weight tiles
-    const int tn = (a.N + kOutN - 1) / kOutN, tm = (a.M + BM - 1) / BM;
-    const int64_t used = (int64_t)tn * tm, share = (used + 7) >> 3;
-    const int64_t li = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
-    if ((int64_t)(blockIdx.x >> 3) >= share || li >= used) return;
-    const int nt = (int)(li / tm), mt = (int)(li - (int64_t)nt * tm);
+    int nt, mt;
+    if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + BM - 1) / BM, nt, mt)) return;
     const int n0 = nt * kOutN;
     const int64_t m0 = (int64_t)mt * BM;
 
@@ -381,34 +596,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
         compute(s & 1);
         if (s + 1 < S) settle((s + 1) & 1);
     }
-    // Epilogue: a wave's sums of 16 tokens at a time through its own part of
-    // the (now free) LDS, out as whole rows of its 16 RB weight rows
-    constexpr int kStride = 16 * RB + 4;   // floats; the padding spreads the tokens over the banks
-    constexpr int kQuads = (GLU ? RB / 2 : RB) * 4;   // four outputs each, per token
-    static_assert(kWaves * 16 * kStride * 4 <= 2 * kRows * BK * 2, "the sums fit the tile buffers");
-    static_assert(64 % kQuads == 0, "whole tokens per round");
-    __syncthreads();
-    float* os = reinterpret_cast<float*>(tile_lds) + wave * 16 * kStride;
-    const int q = lane % kQuads, tok = lane / kQuads;
-    const int col = GLU ? (q >> 2) * 32 + (q & 3) * 4 : q * 4;
-    const int n = n0 + wn * (GLU ? RB / 2 : RB) * 16 + q * 4;
-#pragma unroll
-    for (int j = 0; j < MB; ++j) {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the former tokens are read
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4*>(os + r * kStride + 16 * i + 4 * g) = acc[i][j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int t = tok; t < 16; t += 64 / kQuads) {
-            const int64_t m = m0 + (wm * MB + j) * 16 + t;
-            if (m >= a.M || n >= a.N) continue;
-            const f32x4 z = *reinterpret_cast<const f32x4*>(os + t * kStride + col);
-            const f32x4 up = GLU ? *reinterpret_cast<const f32x4*>(os + t * kStride + col + 16) : z;
-            put4<GLU>(a, m, n, z, up);
-        }
-    }
+    __syncthreads();   // every wave is done with the tile buffers
+    static_assert(kWaves * out_stage_floats<RB>() * 4 <= 2 * kRows * BK * 2, "the sums fit the tile buffers");
+    put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
+                          n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
 }
 
 template <class T, int BM, int BN, int WM, int WN, bool GLU, bool DIRECT>
@@ -448,7 +639,10 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     }
     if (!a.aligned) return launch_tile<T, 64, 64, 2, 2, GLU, false>(a, s);
     const int64_t big = (int64_t)((a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256)) * ((a.M + 255) / 256);
-    if (big >= 128) return launch_tile<T, 256, 256, 4, 2, GLU, true>(a, s);
+    if (big >= 128) {
+        linear_phased_kernel<T, GLU><<<(unsigned)((big + 7) / 8 * 8), 512, kPhSlots * kPhRows * 64, s>>>(a);
+        return hipGetLastError();
+    }
     const int64_t mid = (int64_t)((a.N + (GLU ? 63 : 127)) / (GLU ? 64 : 128)) * ((a.M + 127) / 128);
     if (mid >= 128) return launch_tile<T, 128, 128, 2, 2, GLU, true>(a, s);
     return launch_tile<T, 64, 64, 2, 2, GLU, true>(a, s);
