@@ -57,35 +57,33 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, int dtype, float v
 // Four consecutive values: residual bits, their addition, the store.
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x4 load_quad(const void* p, int64_t i, int dtype) {
-    if (dtype == PW_F32) return *reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(p) + i);
-    const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
-    return u32x4{u.x, u.y, 0u, 0u};
+template <int DT>
+struct QuadOf {
+    typedef uint2 bits;
+    typedef typename std::conditional<DT == PW_BF16, bf16x4, f16x4>::type vec;
+    typedef typename std::conditional<DT == PW_BF16, __bf16, _Float16>::type elem;
+};
+template <>
+struct QuadOf<PW_F32> {
+    typedef u32x4 bits;
+    typedef f32x4 vec;
+    typedef float elem;
+};
+template <int DT>
+__device__ __forceinline__ typename QuadOf<DT>::bits load_quad(const void* p, int64_t i) {
+    return *reinterpret_cast<const typename QuadOf<DT>::bits*>(reinterpret_cast<const typename QuadOf<DT>::elem*>(p) + i);
 }
-__device__ __forceinline__ void add_quad(float (&v)[4], const u32x4& r, int dtype) {
-    if (dtype == PW_F32) {
-        const f32x4 f = __builtin_bit_cast(f32x4, r);
+template <int DT>
+__device__ __forceinline__ void add_quad(float (&v)[4], const typename QuadOf<DT>::bits& r) {
+    const auto f = __builtin_bit_cast(typename QuadOf<DT>::vec, r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += f[e];
-    } else if (dtype == PW_BF16) {
-        const bf16x4 f = __builtin_bit_cast(bf16x4, uint2{r[0], r[1]});
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += (float)f[e];
-    } else {
-        const f16x4 f = __builtin_bit_cast(f16x4, uint2{r[0], r[1]});
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += (float)f[e];
-    }
+    for (int e = 0; e < 4; ++e) v[e] += (float)f[e];
 }
-__device__ __forceinline__ void store_quad(void* p, int64_t i, int dtype, const float (&v)[4]) {
-    if (dtype == PW_F32)
-        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
-    else if (dtype == PW_BF16)
-        *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p) + i) =
-            bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-    else
-        *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(p) + i) =
-            f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+template <int DT>
+__device__ __forceinline__ void store_quad(void* p, int64_t i, const float (&v)[4]) {
+    typedef typename QuadOf<DT>::elem E;
+    *reinterpret_cast<typename QuadOf<DT>::vec*>(reinterpret_cast<E*>(p) + i) =
+        typename QuadOf<DT>::vec{(E)v[0], (E)v[1], (E)v[2], (E)v[3]};
 }
 
 // The activation of n quads (one branch for all of them).
@@ -111,11 +109,11 @@ __device__ __forceinline__ void act_all(float (&v)[N][4], int act) {
 }
 
 // Outputs n .. n + 3 of token m from their sums.
-template <bool GLU>
-__device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, f32x4 z, f32x4 up) {
+template <int DT, bool GLU>
+__device__ __forceinline__ void put4_t(const LinearArgs& a, int64_t m, int n, f32x4 z, f32x4 up) {
     const bool vec = a.vec_out && n + 3 < a.N;
-    u32x4 res = {0u, 0u, 0u, 0u};
-    if (a.residual && vec) res = load_quad(a.residual, m * a.ldr + n, a.out_dtype);
+    typename QuadOf<DT>::bits res{};
+    if (a.residual && vec) res = load_quad<DT>(a.residual, m * a.ldr + n);
     float v[1][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -127,17 +125,23 @@ __device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, f32x
     }
     if constexpr (!GLU) act_all(v, a.act);
     if (vec) {
-        if (a.residual) add_quad(v[0], res, a.out_dtype);
-        store_quad(a.y, m * a.ldy + n, a.out_dtype, v[0]);
+        if (a.residual) add_quad<DT>(v[0], res);
+        store_quad<DT>(a.y, m * a.ldy + n, v[0]);
         return;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (n + e >= a.N) break;
         float o = v[0][e];
-        if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, a.out_dtype);
-        store_out(a.y, m * a.ldy + n + e, a.out_dtype, o);
+        if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, DT);
+        store_out(a.y, m * a.ldy + n + e, DT, o);
     }
+}
+template <bool GLU>
+__device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, const f32x4& z, const f32x4& up) {
+    if (a.out_dtype == PW_F32) put4_t<PW_F32, GLU>(a, m, n, z, up);
+    else if (a.out_dtype == PW_BF16) put4_t<PW_BF16, GLU>(a, m, n, z, up);
+    else put4_t<PW_F16, GLU>(a, m, n, z, up);
 }
 
 // ---- operands ----
@@ -285,18 +289,23 @@ __device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 
 template <int RB>
 __host__ __device__ constexpr int out_stage_floats() { return 16 * (16 * RB + 4); }   // the padding spreads the tokens over the banks
 
-template <int RB, int MB, bool GLU>
-__device__ __forceinline__ void put_tile(const LinearArgs& a, const f32x4 (&acc)[RB][MB], float* os, int n0, int64_t m0) {
+template <int DT, int RB, int MB, bool GLU>
+__device__ __forceinline__ void put_tile_t(const LinearArgs& a, const f32x4 (&acc)[RB][MB], float* os, int n0, int64_t m0) {
     constexpr int kStride = 16 * RB + 4;
     constexpr int kQuads = (GLU ? RB / 2 : RB) * 4;   // four outputs each, per token
-    constexpr int kStep = 64 / kQuads, kIter = 16 / kStep;
-    static_assert(64 % kQuads == 0 && 16 % kStep == 0, "whole tokens per round");
+    // tokens at a time, a power of two (RB = 6 leaves 16 lanes idle)
+    constexpr int kStep = 64 / kQuads >= 16 ? 16 : 64 / kQuads >= 8 ? 8 : 64 / kQuads >= 4 ? 4 : 64 / kQuads >= 2 ? 2 : 1;
+    constexpr int kRounds = 16 / kStep;                // for 16 tokens
+    constexpr int kIter = kRounds < 4 ? kRounds : 4;   // of them in one part
+    constexpr int kParts = kRounds / kIter;
+    static_assert(kStep * kRounds == 16 && kIter * kParts == kRounds, "16 tokens in whole parts");
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int q = lane % kQuads, tok = lane / kQuads;
+    const bool mine = tok < kStep;
     const int col = GLU ? (q >> 2) * 32 + (q & 3) * 4 : q * 4;
-    const int n = n0 + q * 4;
-    // the lane's four columns are the same for every token
-    const bool vec = a.vec_out && n + 3 < a.N;
+    const int n = n0 + q * 4;   // the lane's four columns, for every token
+    const bool whole = a.vec_out && n0 + (GLU ? RB / 2 : RB) * 16 <= a.N && m0 + MB * 16 <= a.M;
+    const bool ahead = whole && a.residual && mine;
     f32x4 bz = {0.f, 0.f, 0.f, 0.f}, bu = bz;
     if (a.bias) {
 #pragma unroll
@@ -307,32 +316,42 @@ __device__ __forceinline__ void put_tile(const LinearArgs& a, const f32x4 (&acc)
             }
         }
     }
-    // one round of the loop serves 16 tokens: the code of the activations is
-    // there once, and all of a round's residual loads are in flight before
-    // the sums are staged
+    // a part's residual is loaded a part ahead, before the stores of the one
+    // between (a wait for a load is a wait for every older store)
+    typename QuadOf<DT>::bits res[kIter], next[kIter];
+    auto fetch = [&](int c) {
+        const int64_t m = m0 + (c / kParts) * 16 + (c % kParts) * kIter * kStep + tok;
+        const int64_t at = m * a.ldr + n;
+#pragma unroll
+        for (int t = 0; t < kIter; ++t) next[t] = load_quad<DT>(a.residual, at + (int64_t)(t * kStep) * a.ldr);
+    };
+    if (ahead) fetch(0);
+    // the loop runs over parts of 16 tokens, so that the code of the
+    // activations is there once
 #pragma unroll 1
-    for (int j = 0; j < MB; ++j) {
-        const int64_t mj = m0 + j * 16 + tok;
+    for (int c = 0; c < MB * kParts; ++c) {
+        if (c % kParts == 0) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the former tokens are read
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int J = 0; J < MB; ++J) {
+                if (J * kParts != c) continue;
+#pragma unroll
+                for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4*>(os + r * kStride + 16 * i + 4 * g) = acc[i][J];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        if (ahead) {
+#pragma unroll
+            for (int t = 0; t < kIter; ++t) res[t] = next[t];
+            if (c + 1 < MB * kParts) fetch(c + 1);
+        }
+        const int t0 = (c % kParts) * kIter * kStep + tok;
         float v[kIter][4];
-        u32x4 res[kIter];
-        if (a.residual && vec) {
-#pragma unroll
-            for (int t = 0; t < kIter; ++t)
-                if (mj + t * kStep < a.M) res[t] = load_quad(a.residual, (mj + t * kStep) * a.ldr + n, a.out_dtype);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the former tokens are read
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int J = 0; J < MB; ++J) {
-            if (J != j) continue;
-#pragma unroll
-            for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4*>(os + r * kStride + 16 * i + 4 * g) = acc[i][J];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int t = 0; t < kIter; ++t) {
-            const float* row = os + (tok + t * kStep) * kStride + col;
+            const float* row = os + min(t0 + t * kStep, 15) * kStride + col;
             const f32x4 z = *reinterpret_cast<const f32x4*>(row) + bz;
             if constexpr (GLU) {
                 const f32x4 up = *reinterpret_cast<const f32x4*>(row + 16) + bu;
@@ -344,24 +363,38 @@ __device__ __forceinline__ void put_tile(const LinearArgs& a, const f32x4 (&acc)
             }
         }
         if constexpr (!GLU) act_all(v, a.act);
+        if (!mine) continue;
+        const int64_t m1 = m0 + (c / kParts) * 16 + t0;
+        if (whole) {
+            if (ahead) {
 #pragma unroll
-        for (int t = 0; t < kIter; ++t) {
-            const int64_t m = mj + t * kStep;
-            if (m >= a.M || n >= a.N) continue;
-            if (vec) {
-                if (a.residual) add_quad(v[t], res[t], a.out_dtype);
-                store_quad(a.y, m * a.ldy + n, a.out_dtype, v[t]);
-            } else {
+                for (int t = 0; t < kIter; ++t) add_quad<DT>(v[t], res[t]);
+            }
+            const int64_t at = m1 * a.ldy + n;
+#pragma unroll
+            for (int t = 0; t < kIter; ++t) store_quad<DT>(a.y, at + (int64_t)(t * kStep) * a.ldy, v[t]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < kIter; ++t) {
+                const int64_t m = m1 + t * kStep;
+                if (m >= a.M) break;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (n + e >= a.N) break;
                     float o = v[t][e];
-                    if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, a.out_dtype);
-                    store_out(a.y, m * a.ldy + n + e, a.out_dtype, o);
+                    if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, DT);
+                    store_out(a.y, m * a.ldy + n + e, DT, o);
                 }
             }
         }
     }
+}
+
+template <int RB, int MB, bool GLU>
+__device__ __forceinline__ void put_tile(const LinearArgs& a, const f32x4 (&acc)[RB][MB], float* os, int n0, int64_t m0) {
+    if (a.out_dtype == PW_F32) put_tile_t<PW_F32, RB, MB, GLU>(a, acc, os, n0, m0);
+    else if (a.out_dtype == PW_BF16) put_tile_t<PW_BF16, RB, MB, GLU>(a, acc, os, n0, m0);
+    else put_tile_t<PW_F16, RB, MB, GLU>(a, acc, os, n0, m0);
 }
 
 // Tile of this workgroup, or false past the last. Each XCD (every eighth
@@ -381,60 +414,67 @@ __device__ __forceinline__ bool tile_of(int tn, int tm, int& nt, int& mt) {
     return true;
 }
 
-// Large products: 256 weight rows x 256 tokens, 8 waves of 128 x 64 each, K
-// in stages of 32 (64-byte LDS rows) through four LDS slots.
+// Large products: 32 RB weight rows x 64 MB tokens (256 x 256 at most), 8
+// waves (2 x 4) of 16 RB x 16 MB each, K in stages of 64 (128-byte LDS rows)
+// through two LDS slots.
 //
-// The two waves of a SIMD take turns: a stage is a phase of operand reads
-// (12 of 16 bytes a lane, and the copies of the stage after the next two
-// into their slot) and a phase of 32 matrix instructions; waves 4 .. 7 run
-// one phase behind waves 0 .. 3, so that one wave of each SIMD multiplies
-// while the other reads. Phases end at barriers. With stage s read in phases
-// 2 s and 2 s + 1, its slot is free from phase 2 s + 2 on, when the first
-// waves copy stage s + 4 into it; those copies have to be whole before phase
-// 2 s + 8, and every wave waits for its own at the end of its read phase of
-// stage s + 3, two later stages still on their way (8 copies a thread).
-// Copies past the last stage read zeros (out of the buffer's bounds) and
-// keep the counts alike.
+// The two waves of a SIMD take turns. Half a stage is a phase of operand
+// reads (RB + MB of 16 bytes a lane) and a phase of RB MB matrix
+// instructions; waves 4 .. 7 run one phase behind waves 0 .. 3, so that one
+// wave of each SIMD multiplies while the other reads. Phases end at
+// barriers. Stage s is read in phases 4 s .. 4 s + 3; the other slot, read up
+// to phase 4 s - 1, takes the copies of stage s + 1 meanwhile: each wave
+// starts its own among its first matrix instructions of the stage (issued
+// with the reads they delayed these: 177k cycles for 64 stages of a 256 x 256
+// tile, 163k so; the matrix instructions alone take 131k) and waits for them
+// by the end of phase 4 s + 3 (the first four waves multiply there, the
+// others read). Copies past the last stage read zeros (out of the buffer's
+// bounds).
 //
-// A row's 16-byte chunk c lies at position c ^ (row / 4 % 4): the 16 rows
-// of an operand read fall on different banks.
-constexpr int kPhRows = 512, kPhSlots = 4;
-template <class T, bool GLU>
+// A row's 16-byte chunk c lies at position c ^ (row % 8): the rows of an
+// operand read fall on different banks (no conflicts counted; 64-byte rows
+// had one cycle in three).
+template <class T, int RB, int MB, bool GLU>
 __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
-    constexpr int RB = 8, MB = 4, kK = 32;
-    constexpr int kOutN = GLU ? 128 : 256;
+    constexpr int BN = 32 * RB, BM = 64 * MB, kRows = BN + BM;
+    constexpr int kOutN = GLU ? BN / 2 : BN;
+    constexpr int QW = BN / 64, QX = BM / 64;   // copies per thread and stage
     extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     int nt, mt;
-    if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + 255) / 256, nt, mt)) return;
+    if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + BM - 1) / BM, nt, mt)) return;
     const int n0 = nt * kOutN;
-    const int64_t m0 = (int64_t)mt * 256;
-    // copies: 4 a thread and stage, each instruction of a wave 16 rows; rows
-    // 128 j' + 16 wave + lane / 4 of the weights (j = 0, 1) and tokens
-    const int crow = lane >> 2, chunk = (lane & 3) ^ ((crow >> 2) & 3);
+    const int64_t m0 = (int64_t)mt * BM;
+    // a wave's copy covers 8 rows: 64 j + 8 wave + lane / 8 of the weights,
+    // then of the tokens
+    const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
     const uint16_t* wbase = reinterpret_cast<const uint16_t*>(a.w) + (int64_t)n0 * a.ldw;
     const uint16_t* xbase = reinterpret_cast<const uint16_t*>(a.x) + m0 * a.ldx;
     // SwiGLU: the tile's blocks of 16 rows are gate and up rows in turn (a
-    // wave's copies are always one kind: 16 wave and 128 + 16 wave)
-    const bool up = GLU && (wave & 1);
+    // wave copies one kind)
+    const bool up = GLU && (wave & 2);
     const auto rw = make_rsrc(wbase + (up ? (int64_t)a.N * a.ldw : 0)), rx = make_rsrc(xbase);
-    uint32_t off[4];
+    uint32_t off[QW + QX];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int lr = 128 * j + 16 * wave + crow;
+    for (int j = 0; j < QW; ++j) {
+        const int lr = 64 * j + 8 * wave + crow;
         const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
         off[j] = n0 + wr < a.N ? (uint32_t)(wr * a.ldw + 8 * chunk) * 2u : kOutside;
-        off[2 + j] = m0 + lr < a.M ? (uint32_t)(lr * a.ldx + 8 * chunk) * 2u : kOutside;
+    }
+#pragma unroll
+    for (int j = 0; j < QX; ++j) {
+        const int lr = 64 * j + 8 * wave + crow;
+        off[QW + j] = m0 + lr < a.M ? (uint32_t)(lr * a.ldx + 8 * chunk) * 2u : kOutside;
     }
     auto copy = [&](int s) {
-        const int k0 = s * kK;
+        const int k0 = s * BK;
         const bool in = k0 + 8 * chunk < a.K;
-        uint16_t* dst = tile_lds + (s & (kPhSlots - 1)) * kPhRows * kK;
+        uint16_t* dst = tile_lds + (s & 1) * kRows * BK + 8 * wave * BK;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            copy_to_lds(j < 2 ? rw : rx, dst + (128 * j + 16 * wave) * kK, in ? off[j] : kOutside, in_bytes(k0, a.K));
+        for (int j = 0; j < QW + QX; ++j)
+            copy_to_lds(j < QW ? rw : rx, dst + 64 * j * BK, in ? off[j] : kOutside, in_bytes(k0, a.K));
     };
     f32x4 acc[RB][MB];
 #pragma unroll
@@ -442,41 +482,63 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int wn = wave & 1, wm = wave >> 1;
-    const int pos = r * 4 + (g ^ ((r >> 2) & 3));
-    const int S = (a.K + kK - 1) / kK;
+    const bool late = wave >= 4;
+    const int S = (a.K + BK - 1) / BK;
     copy(0);
-    copy(1);
-    copy(2);
-    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-    if (wave >= 4) asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (late) asm volatile("s_barrier" ::: "memory");
     for (int s = 0; s < S; ++s) {
-        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + (s & (kPhSlots - 1)) * kPhRows * kK) + pos;
-        u32x4 fw[RB], fx[MB];
 #pragma unroll
-        for (int j = 0; j < MB; ++j) fx[j] = base[(256 + (wm * MB + j) * 16) * 4];
+        for (int h = 0; h < 2; ++h) {
+            const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + (s & 1) * kRows * BK) + r * 8 +
+                                ((4 * h + g) ^ (r & 7));
+            u32x4 fw[RB], fx[MB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) fw[i] = base[(wn * RB + i) * 64];
-        copy(s + 3);
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
+            for (int j = 0; j < MB; ++j) fx[j] = base[(BN + (wm * MB + j) * 16) * 8];
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
+            for (int i = 0; i < RB; ++i) fw[i] = base[(wn * RB + i) * 128];
+            __builtin_amdgcn_sched_barrier(0);
+            if (h == 1 && late) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            if (h == 0) copy(s + 1);
 #pragma unroll
-            for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
-        __builtin_amdgcn_s_setprio(0);
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
+            if (h == 0) {
+                // a copy after every second matrix instruction
+#pragma unroll
+                for (int q = 0; q < QW + QX; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x10, 1, 0);
+                }
+            }
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (h == 1 && !late) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            asm volatile("s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
-    // the copies past the last stage land before the LDS is used again
-    if (wave < 4) asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // the early waves' last barrier pairs with the late ones' last phase;
+    // every copy has landed before the LDS is used again
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (!late) asm volatile("s_barrier" ::: "memory");
     __syncthreads();
-    static_assert(8 * out_stage_floats<RB>() * 4 <= kPhSlots * kPhRows * kK * 2, "the sums fit the slots");
+    static_assert(8 * out_stage_floats<RB>() * 4 <= 2 * kRows * BK * 2, "the sums fit the slots");
     put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
                           n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
+}
+
+template <class T, int RB, int MB, bool GLU>
+hipError_t launch_phased(const LinearArgs& a, hipStream_t s) {
+    constexpr int kOutN = GLU ? 16 * RB : 32 * RB, BM = 64 * MB;
+    const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
+    linear_phased_kernel<T, RB, MB, GLU>
+        <<<(unsigned)((tiles + 7) / 8 * 8), 512, (size_t)2 * (32 * RB + BM) * BK * 2, s>>>(a);
+    return hipGetLastError();
 }
 
 // Tile: BN weight rows x BM tokens, WN x WM waves, K in steps of 64 through
@@ -638,10 +700,13 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
         return launch_skinny<T, 4, 4, GLU>(a, waves, s);
     }
     if (!a.aligned) return launch_tile<T, 64, 64, 2, 2, GLU, false>(a, s);
-    const int64_t big = (int64_t)((a.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256)) * ((a.M + 255) / 256);
-    if (big >= 128) {
-        linear_phased_kernel<T, GLU><<<(unsigned)((big + 7) / 8 * 8), 512, kPhSlots * kPhRows * 64, s>>>(a);
-        return hipGetLastError();
+    const int64_t cols = GLU ? 2ll * a.N : a.N;
+    auto tiles = [&](int64_t bn, int64_t bm) { return (cols + bn - 1) / bn * ((a.M + bm - 1) / bm); };
+    const int64_t t84 = tiles(256, 256);
+    if (t84 >= 128) {
+        const int64_t r84 = (t84 + 255) / 256 * 256, r64 = (tiles(192, 256) + 255) / 256 * 200;
+        if (r64 < r84) return launch_phased<T, 6, 4, GLU>(a, s);
+        return launch_phased<T, 8, 4, GLU>(a, s);
     }
     const int64_t mid = (int64_t)((a.N + (GLU ? 63 : 127)) / (GLU ? 64 : 128)) * ((a.M + 127) / 128);
     if (mid >= 128) return launch_tile<T, 128, 128, 2, 2, GLU, true>(a, s);
