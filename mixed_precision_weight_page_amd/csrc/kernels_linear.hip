@@ -149,11 +149,9 @@ __device__ __forceinline__ void put4(const LinearArgs& a, int64_t m, int n, cons
 // 8 consecutive K values from p, which need not be aligned (the loads are
 // declared with the element's alignment); left: values of the row from p on,
 // zeros past them
-struct __attribute__((packed, aligned(2))) Chunk {
-    u32x4 v;
-};
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ u32x4 load_chunk(const uint16_t* p, int left) {
-    if (left >= 8) return reinterpret_cast<const Chunk*>(p)->v;
+    if (left >= 8) return *reinterpret_cast<const u32x4_any*>(p);
     u32x4 u = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -161,79 +159,35 @@ __device__ __forceinline__ u32x4 load_chunk(const uint16_t* p, int left) {
     return u;
 }
 
+constexpr int BK = 64;   // K values per step: 128-byte rows in LDS
+constexpr uint32_t kOutside = 0x80000000u;   // buffer offset past every record: reads 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32) |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), (short)0, 0x7fffffff, 0x00020000);
+}
+
+// 16 bytes per lane from the buffer to LDS, lane i's to dst + 16 i (device
+// pass only: the host pass does not know the builtin)
+__device__ __forceinline__ void copy_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, uint16_t* dst, uint32_t off, int soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 16, (int)off, soff, 0, 0);
+#endif
+}
+
+// byte offset of K value k0, 0 past the end (the lanes are out of bounds there)
+__device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 : 0; }
+
 // ---- few tokens ----
 
-// Workgroup: RB blocks of 16 weight rows (with SwiGLU the same RB / 2 blocks
-// of gate and of up rows), MB blocks of 16 tokens, the K range dealt to its
-// waves in pieces of 64: neighbouring waves read neighbouring 128 bytes of
-// every row, straight into MFMA operands, one piece ahead. The waves' sums
-// meet in LDS.
-template <class T, int RB, int MB, bool GLU>
-__global__ __launch_bounds__(RB * MB > 4 ? 256 : 1024) void linear_skinny_kernel(LinearArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float part[];   // [waves][RB][MB][64 lanes][4]
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
+// The sums of a workgroup's waves (each over its own pieces of K) through
+// LDS, added in wave order, and out.
+template <int RB, int MB, bool GLU>
+__device__ __forceinline__ void join_waves(const LinearArgs& a, const f32x4 (&acc)[RB][MB], float* part, int n0, int m0) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
-    const int n0 = blockIdx.x * kRowsOut, m0 = blockIdx.y * 16 * MB;
-    // rows past the end repeat the last one; their sums are dropped
-    const uint16_t* wp[RB];
-    const uint16_t* xp[MB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const int blk = GLU ? b >> 1 : b;
-        const int64_t row = min(n0 + 16 * blk + r, a.N - 1) + (GLU && (b & 1) ? (int64_t)a.N : 0);
-        wp[b] = reinterpret_cast<const uint16_t*>(a.w) + row * a.ldw + 8 * g;
-    }
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-        xp[b] = reinterpret_cast<const uint16_t*>(a.x) + (int64_t)min(m0 + 16 * b + r, a.M - 1) * a.ldx + 8 * g;
-    f32x4 acc[RB][MB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    struct Piece {
-        u32x4 w[RB][2], x[MB][2];
-    };
-    auto load = [&](Piece& p, int k) {
-        if (k + 64 <= a.K) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int b = 0; b < RB; ++b) p.w[b][h] = reinterpret_cast<const Chunk*>(wp[b] + k + 32 * h)->v;
-#pragma unroll
-                for (int b = 0; b < MB; ++b) p.x[b][h] = reinterpret_cast<const Chunk*>(xp[b] + k + 32 * h)->v;
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int left = a.K - (k + 32 * h + 8 * g);
-#pragma unroll
-                for (int b = 0; b < RB; ++b) p.w[b][h] = load_chunk(wp[b] + k + 32 * h, left);
-#pragma unroll
-                for (int b = 0; b < MB; ++b) p.x[b][h] = load_chunk(xp[b] + k + 32 * h, left);
-            }
-        }
-    };
-    auto multiply = [&](const Piece& p) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(p.w[i][h], p.x[j][h], acc[i][j]);
-    };
-    const int step = 64 * waves;
-    Piece p0, p1;
-    int k = 64 * wave;
-    if (k < a.K) load(p0, k);
-    for (; k < a.K; k += 2 * step) {
-        if (k + step < a.K) load(p1, k + step);
-        multiply(p0);
-        if (k + 2 * step < a.K) load(p0, k + 2 * step);
-        if (k + step < a.K) multiply(p1);
-    }
     f32x4* mine = reinterpret_cast<f32x4*>(part) + (int64_t)wave * RB * MB * 64 + lane;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -260,28 +214,170 @@ __global__ __launch_bounds__(RB * MB > 4 ? 256 : 1024) void linear_skinny_kernel
     }
 }
 
+// Workgroup: RB blocks of 16 weight rows (with SwiGLU the same RB / 2 blocks
+// of gate and of up rows), MB blocks of 16 tokens, the K range dealt to its
+// waves in pieces of 64: neighbouring waves read neighbouring 128 bytes of
+// every row, straight into MFMA operands, D pieces in flight per wave. The
+// waves' sums meet in LDS. Weights are read once: non-temporal loads keep
+// the tokens in the caches.
+template <class T, int RB, int MB, int D, bool GLU>
+__global__ __launch_bounds__(RB * MB > 4 ? 256 : 1024) void linear_skinny_kernel(LinearArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float part[];   // [waves][RB][MB][64 lanes][4]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
+    const int n0 = blockIdx.x * kRowsOut, m0 = blockIdx.y * 16 * MB;
+    // rows past the end repeat the last one; their sums are dropped
+    const uint16_t* wp[RB];
+    const uint16_t* xp[MB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int blk = GLU ? b >> 1 : b;
+        const int64_t row = min(n0 + 16 * blk + r, a.N - 1) + (GLU && (b & 1) ? (int64_t)a.N : 0);
+        wp[b] = reinterpret_cast<const uint16_t*>(a.w) + row * a.ldw + 16 * g;
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        xp[b] = reinterpret_cast<const uint16_t*>(a.x) + (int64_t)min(m0 + 16 * b + r, a.M - 1) * a.ldx + 16 * g;
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Piece {
+        u32x4 w[RB][2], x[MB][2];
+    };
+    auto load = [&](Piece& p, int i) {   // the wave's i-th piece, a whole one
+        const int k = 64 * (wave + waves * i);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                p.w[b][h] = *reinterpret_cast<const u32x4_any*>(wp[b] + k + 8 * h);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) p.x[b][h] = *reinterpret_cast<const u32x4_any*>(xp[b] + k + 8 * h);
+        }
+    };
+    auto multiply = [&](const Piece& p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(p.w[i][h], p.x[j][h], acc[i][j]);
+    };
+    const int whole = a.K >> 6;   // whole pieces, dealt in turn
+    const int n = whole > wave ? (whole - wave + waves - 1) / waves : 0;
+    Piece ring[D];
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (j < n) load(ring[j], j);
+    int i = 0;
+    for (; i + 2 * D <= n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            multiply(ring[j]);
+            load(ring[j], i + D + j);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+        if (i + j < n) multiply(ring[j]);
+        if (i + D + j < n) load(ring[j], i + D + j);
+    }
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (i + D + j < n) multiply(ring[j]);
+    if ((a.K & 63) && whole % waves == wave) {   // the last, partial piece
+        Piece p;
+        const int k = 64 * whole;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int left = a.K - (k + 8 * h + 16 * g);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) p.w[b][h] = load_chunk(wp[b] + k + 8 * h, left);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) p.x[b][h] = load_chunk(xp[b] + k + 8 * h, left);
+        }
+        multiply(p);
+    }
+    join_waves<RB, MB, GLU>(a, acc, part, n0, m0);
+}
+
+// The same product for 16-byte aligned rows, the pieces through LDS: a wave
+// copies its own pieces (8 whole 128-byte row parts per instruction) into a
+// ring of D slots that no other wave touches, so nothing but its own counter
+// of copies is waited for, and what is in flight takes no registers.
+template <class T, int RB, int MB, int D, bool GLU>
+__global__ __launch_bounds__(1024) void linear_stream_kernel(LinearArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint16_t ring_lds[];   // [waves][D][RB + MB][16 rows][64]
+    constexpr int kBlock = 16 * BK, kSlot = (RB + MB) * kBlock;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
+    const int n0 = blockIdx.x * kRowsOut, m0 = blockIdx.y * 16 * MB;
+    const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
+    const uint16_t* wbase = reinterpret_cast<const uint16_t*>(a.w) + (int64_t)n0 * a.ldw;
+    const auto rw = make_rsrc(wbase), ru = make_rsrc(wbase + (GLU ? (int64_t)a.N * a.ldw : 0));
+    const auto rx = make_rsrc(reinterpret_cast<const uint16_t*>(a.x) + (int64_t)m0 * a.ldx);
+    uint32_t off[RB + MB][2];
+#pragma unroll
+    for (int b = 0; b < RB + MB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 16 * (b >= RB ? b - RB : GLU ? b >> 1 : b) + 8 * h + crow;
+            const bool in = b >= RB ? m0 + row < a.M : n0 + row < a.N;
+            off[b][h] = in ? (uint32_t)(row * (b >= RB ? a.ldx : a.ldw) + 8 * chunk) * 2u : kOutside;
+        }
+    const int total = (a.K + BK - 1) / BK;
+    const int n = total > wave ? (total - wave + waves - 1) / waves : 0;
+    uint16_t* ring = ring_lds + wave * D * kSlot;
+    auto copy = [&](int i, int slot) {   // piece i of this wave (past the last: zeros, no memory touched)
+        const int k0 = BK * (wave + waves * i);
+        const bool in = k0 + 8 * chunk < a.K;
+#pragma unroll
+        for (int b = 0; b < RB + MB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                copy_to_lds(b >= RB ? rx : GLU && (b & 1) ? ru : rw, ring + slot * kSlot + b * kBlock + 8 * h * BK,
+                            in ? off[b][h] : kOutside, in_bytes(k0, a.K));
+    };
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < D; ++j) copy(j, j);
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (RB + MB) * (D - 1)) : "memory");
+        const u32x4* base = reinterpret_cast<const u32x4*>(ring + slot * kSlot) + r * 8;
+        u32x4 f[RB + MB][2];
+#pragma unroll
+        for (int b = 0; b < RB + MB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f[b][h] = base[b * 128 + ((4 * h + g) ^ (r & 7))];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read, before the slot is written again
+        __builtin_amdgcn_sched_barrier(0);
+        copy(i + D, slot);
+        slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < RB; ++p)
+#pragma unroll
+                for (int q = 0; q < MB; ++q) acc[p][q] = mma<T>(f[p][h], f[RB + q][h], acc[p][q]);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();   // the rings are done with
+    join_waves<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(ring_lds), n0, m0);
+}
+
 // ---- many tokens ----
 
-constexpr int BK = 64;   // K values per step: 128-byte rows in LDS
-constexpr uint32_t kOutside = 0x80000000u;   // buffer offset past every record: reads 0
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint64_t u = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32) |
-                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), (short)0, 0x7fffffff, 0x00020000);
-}
-
-// 16 bytes per lane from the buffer to LDS, lane i's to dst + 16 i (device
-// pass only: the host pass does not know the builtin)
-__device__ __forceinline__ void copy_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, uint16_t* dst, uint32_t off, int soff) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 16, (int)off, soff, 0, 0);
-#endif
-}
-
-// byte offset of K value k0, 0 past the end (the lanes are out of bounds there)
-__device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 : 0; }
 
 // Epilogue of a wave's tile: the sums of 16 tokens at a time through the
 // wave's own part of the (free) LDS, out as whole rows of its 16 RB weight
@@ -675,12 +771,21 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <class T, int RB, int MB, bool GLU>
+template <class T, int RB, int MB, int D, bool GLU>
+hipError_t launch_stream(const LinearArgs& a, int waves, hipStream_t s) {
+    constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
+    const dim3 grid((unsigned)((a.N + kRowsOut - 1) / kRowsOut), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+    const size_t lds = std::max((size_t)waves * D * (RB + MB) * 2048, (size_t)waves * RB * MB * 1024);
+    linear_stream_kernel<T, RB, MB, D, GLU><<<grid, 64 * waves, lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <class T, int RB, int MB, int D, bool GLU>
 hipError_t launch_skinny(const LinearArgs& a, int waves, hipStream_t s) {
     constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
     const dim3 grid((unsigned)((a.N + kRowsOut - 1) / kRowsOut), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
     const size_t lds = (size_t)waves * RB * MB * 1024;
-    linear_skinny_kernel<T, RB, MB, GLU><<<grid, 64 * waves, lds, s>>>(a);
+    linear_skinny_kernel<T, RB, MB, D, GLU><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
 }
 
@@ -690,14 +795,35 @@ template <class T, bool GLU>
 hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     if (a.M <= kSkinnyTokens) {
         const int mb = (a.M + 15) / 16;
-        const int64_t rows = GLU ? 2ll * a.N : a.N;
-        int waves = 4;
-        const int64_t blocks = (rows + 31) / 32 * (rows <= 8192 ? mb : 1);
-        while (waves < 16 && blocks * waves < 4096 && waves * 64 < a.K) waves *= 2;
-        if (mb == 1 || rows <= 8192) return launch_skinny<T, 2, 1, GLU>(a, waves, s);
-        waves = std::min(waves, 4);
-        if (mb == 2) return launch_skinny<T, 4, 2, GLU>(a, waves, s);
-        return launch_skinny<T, 4, 4, GLU>(a, waves, s);
+        const int64_t b32 = ((GLU ? 2ll * a.N : a.N) + 31) / 32;   // blocks of 32 weight rows
+        auto waves_for = [&](int64_t blocks) {
+            int w = 4;
+            while (w < 16 && blocks * w < 3072 && w * BK < a.K) w *= 2;
+            return w;
+        };
+        // few rows: a workgroup per 16 of them and per 16 tokens, up to 16
+        // waves along K (64 x 128 x 2048: 6.9 us; 32 rows each 8.5 us. 1 x
+        // 4096 x 14336: 22.5 us, through LDS 23.3 us)
+        if (b32 * mb < 256) {
+            if constexpr (GLU) return launch_skinny<T, 2, 1, 3, GLU>(a, waves_for(b32 * mb), s);
+            else return launch_skinny<T, 1, 1, 4, GLU>(a, waves_for(2 * b32 * mb), s);
+        }
+        if (!a.aligned) {
+            if (mb == 1) return launch_skinny<T, 2, 1, 3, GLU>(a, waves_for(b32), s);
+            if (mb == 2) return launch_skinny<T, 4, 2, 2, GLU>(a, 4, s);
+            return launch_skinny<T, 4, 4, 2, GLU>(a, 4, s);
+        }
+        // through LDS: 16 x 14336 x 4096 SwiGLU 44.7 us (straight into
+        // registers 49.9 us), 32 tokens 49.6 (54.6), 64 tokens 65.3 (71.9).
+        // More than 32 tokens share a workgroup's weights only where the rows
+        // fill the GPU (64 x 4096 x 14336: 38.8 us, 51.4 us shared), up to 32
+        // take 16 rows where 32 do not (17 x 4096 x 14336: 28.4 and 34.3 us).
+        const int w = std::min(4, std::max(1, (a.K + BK - 1) / BK));
+        if (mb == 1) return launch_stream<T, 2, 1, 2, GLU>(a, w, s);
+        if constexpr (!GLU)
+            if (mb == 2 && b32 <= 256) return launch_stream<T, 1, 2, 2, GLU>(a, w, s);
+        if (mb == 2 || b32 <= 256) return launch_stream<T, 2, 2, 2, GLU>(a, w, s);
+        return launch_stream<T, 2, 4, 2, GLU>(a, w, s);
     }
     if (!a.aligned) return launch_tile<T, 64, 64, 2, 2, GLU, false>(a, s);
     const int64_t cols = GLU ? 2ll * a.N : a.N;
