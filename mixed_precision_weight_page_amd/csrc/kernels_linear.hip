@@ -637,22 +637,17 @@ hipError_t launch_phased(const LinearArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tile: BN weight rows x BM tokens, WN x WM waves, K in steps of 64 through
-// two LDS buffers. A row's 16-byte chunk c lies at chunk position
-// c ^ (row % 8), which spreads the 16 rows of an operand read over the
-// banks. DIRECT: the rows go from memory to LDS without registers (needs
-// 16-byte aligned rows; rows and K chunks past the end read as zeros by the
-// buffer's bounds check); else through registers, with unaligned loads.
-// SwiGLU: the tile's blocks of 16 rows are gate and up rows in turn, so one
-// lane holds both sums of its outputs.
-template <class T, int BM, int BN, int WM, int WN, bool GLU, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a) {
-    constexpr int kThr = 64 * WM * WN, kWaves = WM * WN;
+// Products too small to fill the GPU with those tiles: BN weight rows x BM
+// tokens, WN x WM waves, K in steps of 64 through a ring of D LDS slots, one
+// barrier a step, so that D - 2 steps' copies are on their way while one is
+// multiplied. Rows, chunks and copies as above.
+template <class T, int BM, int BN, int WM, int WN, int D, bool GLU>
+__global__ __launch_bounds__(64 * WM * WN) void linear_ring_kernel(LinearArgs a) {
+    constexpr int kWaves = WM * WN, kRows = BN + BM;
     constexpr int RB = BN / WN / 16, MB = BM / WM / 16;   // blocks of a wave's tile
-    constexpr int kRows = BN + BM;                          // LDS rows: weights, then tokens
     constexpr int kOutN = GLU ? BN / 2 : BN;
-    constexpr int QW = BN * 8 / kThr, QX = BM * 8 / kThr;   // 16-byte chunks per thread and step
-    static_assert(BN * 8 % kThr == 0 && BM * 8 % kThr == 0, "whole chunks per thread");
+    constexpr int QW = BN / 8 / kWaves, QX = BM / 8 / kWaves;   // copies per thread and step
+    static_assert(BN % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole copies");
     extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -661,61 +656,34 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + BM - 1) / BM, nt, mt)) return;
     const int n0 = nt * kOutN;
     const int64_t m0 = (int64_t)mt * BM;
-
-    // this thread's chunks: LDS row (j kWaves + wave) 8 + lane / 8, chunk
-    // position lane % 8, hence chunk (lane % 8) ^ (lane / 8) of the row
-    const int cpos = lane & 7, crow = lane >> 3, chunk = cpos ^ crow;
+    const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
     const uint16_t* wbase = reinterpret_cast<const uint16_t*>(a.w) + (int64_t)n0 * a.ldw;
-    const uint16_t* xbase = reinterpret_cast<const uint16_t*>(a.x) + m0 * a.ldx;
-    const uint16_t* ubase = wbase + (GLU ? (int64_t)a.N * a.ldw : 0);
-    const auto rw = make_rsrc(wbase), rx = make_rsrc(xbase), ru = make_rsrc(ubase);
-    uint32_t ow[QW], ox[QX];   // byte offsets of the chunks at K = 0
+    const auto rw = make_rsrc(wbase), ru = make_rsrc(wbase + (GLU ? (int64_t)a.N * a.ldw : 0));
+    const auto rx = make_rsrc(reinterpret_cast<const uint16_t*>(a.x) + m0 * a.ldx);
+    uint32_t off[QW + QX];
 #pragma unroll
     for (int j = 0; j < QW; ++j) {
         const int lr = (j * kWaves + wave) * 8 + crow;
-        const int row = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
-        ow[j] = n0 + row < a.N ? (uint32_t)(row * a.ldw + 8 * chunk) * 2u : kOutside;
+        const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
+        off[j] = n0 + wr < a.N ? (uint32_t)(wr * a.ldw + 8 * chunk) * 2u : kOutside;
     }
 #pragma unroll
     for (int j = 0; j < QX; ++j) {
-        const int row = (j * kWaves + wave) * 8 + crow;
-        ox[j] = m0 + row < a.M ? (uint32_t)(row * a.ldx + 8 * chunk) * 2u : kOutside;
+        const int lr = (j * kWaves + wave) * 8 + crow;
+        off[QW + j] = m0 + lr < a.M ? (uint32_t)(lr * a.ldx + 8 * chunk) * 2u : kOutside;
     }
-    const int S = (a.K + BK - 1) / BK;
-    u32x4 reg[DIRECT ? 1 : QW + QX];
-    // gate or up rows: LDS rows (j kWaves + wave) 8 .. + 7 lie in one block of 16
-    auto is_up = [&](int j) { return GLU && ((((j * kWaves + wave) * 8) >> 4) & 1); };
-    auto fetch = [&](int s, int buf) {
+    auto copy = [&](int s, int slot) {
         const int k0 = s * BK;
         const bool in = k0 + 8 * chunk < a.K;
-        if constexpr (DIRECT) {
-            uint16_t* dst = tile_lds + buf * kRows * BK;
+        uint16_t* dst = tile_lds + slot * kRows * BK;
 #pragma unroll
-            for (int j = 0; j < QW; ++j)
-                copy_to_lds(is_up(j) ? ru : rw, dst + (j * kWaves + wave) * 8 * BK, in ? ow[j] : kOutside, k0 * 2);
-#pragma unroll
-            for (int j = 0; j < QX; ++j)
-                copy_to_lds(rx, dst + (BN + (j * kWaves + wave) * 8) * BK, in ? ox[j] : kOutside, k0 * 2);
-        } else {
-            const int left = a.K - (k0 + 8 * chunk);
-#pragma unroll
-            for (int j = 0; j < QW; ++j)
-                reg[j] = (ow[j] != kOutside && left > 0)
-                             ? load_chunk((is_up(j) ? ubase : wbase) + (ow[j] >> 1) + k0, left) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int j = 0; j < QX; ++j)
-                reg[QW + j] = (ox[j] != kOutside && left > 0) ? load_chunk(xbase + (ox[j] >> 1) + k0, left)
-                                                              : u32x4{0u, 0u, 0u, 0u};
+        for (int j = 0; j < QW; ++j) {
+            const bool up = GLU && ((((j * kWaves + wave) * 8) >> 4) & 1);
+            copy_to_lds(up ? ru : rw, dst + (j * kWaves + wave) * 8 * BK, in ? off[j] : kOutside, in_bytes(k0, a.K));
         }
-    };
-    auto settle = [&](int buf) {   // registers to LDS
-        if constexpr (!DIRECT) {
-            u32x4* dst = reinterpret_cast<u32x4*>(tile_lds + buf * kRows * BK) + lane;
 #pragma unroll
-            for (int j = 0; j < QW; ++j) dst[(j * kWaves + wave) * 64] = reg[j];
-#pragma unroll
-            for (int j = 0; j < QX; ++j) dst[BN * 8 + (j * kWaves + wave) * 64] = reg[QW + j];
-        }
+        for (int j = 0; j < QX; ++j)
+            copy_to_lds(rx, dst + (BN + (j * kWaves + wave) * 8) * BK, in ? off[QW + j] : kOutside, in_bytes(k0, a.K));
     };
     f32x4 acc[RB][MB];
 #pragma unroll
@@ -723,52 +691,124 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int wn = wave % WN, wm = wave / WN;
-    // operand chunk of K group h: position (4 h + g) ^ (row % 8)
-    int pos[2];
+    const int S = (a.K + BK - 1) / BK;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) pos[h] = r * 8 + ((4 * h + g) ^ (r & 7));
-    auto compute = [&](int buf) {
-        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + buf * kRows * BK);
-        const u32x4* wl = base + wn * RB * 128;
-        const u32x4* xl = base + BN * 8 + wm * MB * 128;
+    for (int j = 0; j < D - 1; ++j) copy(j, j);
+    int slot = 0;
+    for (int s = 0; s < S; ++s) {
+        // step s is whole (this wave's part, then everyone's), and everyone
+        // has read the slot before it, which takes step s + D - 1
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((QW + QX) * (D - 2)) : "memory");
+        copy(s + D - 1, slot == 0 ? D - 1 : slot - 1);
+        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + slot * kRows * BK) + r * 8;
+        u32x4 fw[2][RB], fx[2][MB];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const int pos = (4 * h + g) ^ (r & 7);
+#pragma unroll
+            for (int j = 0; j < MB; ++j) fx[h][j] = base[(BN + (wm * MB + j) * 16) * 8 + pos];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) fw[h][i] = base[(wn * RB + i) * 128 + pos];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[h][i], fx[h][j], acc[i][j]);
+        slot = slot + 1 == D ? 0 : slot + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();   // every wave is done with the slots
+    static_assert(kWaves * out_stage_floats<RB>() * 4 <= D * kRows * BK * 2, "the sums fit the slots");
+    put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
+                          n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
+}
+
+template <class T, int BM, int BN, int WM, int WN, int D, bool GLU>
+hipError_t launch_ring(const LinearArgs& a, hipStream_t s) {
+    constexpr int kOutN = GLU ? BN / 2 : BN;
+    const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
+    linear_ring_kernel<T, BM, BN, WM, WN, D, GLU>
+        <<<(unsigned)((tiles + 7) / 8 * 8), 64 * WM * WN, (size_t)D * (BN + BM) * BK * 2, s>>>(a);
+    return hipGetLastError();
+}
+
+// Rows of any alignment: 64 weight rows x 64 tokens, 2 x 2 waves, K in steps
+// of 64 through two LDS buffers; the rows go through registers, loaded a step
+// ahead with unaligned loads. LDS layout as above.
+template <class T, bool GLU>
+__global__ __launch_bounds__(256) void linear_any_kernel(LinearArgs a) {
+    constexpr int RB = 2, MB = 2, kRows = 128;
+    constexpr int kOutN = GLU ? 32 : 64;
+    extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    int nt, mt;
+    if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + 63) / 64, nt, mt)) return;
+    const int n0 = nt * kOutN;
+    const int64_t m0 = (int64_t)mt * 64;
+    // this thread's chunks: LDS rows 32 j + 8 wave + lane / 8 (j < 2 weights,
+    // then tokens), position lane % 8
+    const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
+    const uint16_t* src[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int lr = 32 * (j & 1) + 8 * wave + crow;
+        if (j < 2) {
+            const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
+            const int64_t row = (GLU && ((lr >> 4) & 1) ? (int64_t)a.N : 0) + n0 + wr;
+            src[j] = n0 + wr < a.N ? reinterpret_cast<const uint16_t*>(a.w) + row * a.ldw + 8 * chunk : nullptr;
+        } else {
+            src[j] = m0 + lr < a.M ? reinterpret_cast<const uint16_t*>(a.x) + (m0 + lr) * a.ldx + 8 * chunk : nullptr;
+        }
+    }
+    const int S = (a.K + BK - 1) / BK;
+    u32x4 reg[4];
+    auto fetch = [&](int s) {
+        const int left = a.K - (s * BK + 8 * chunk);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            reg[j] = src[j] && left > 0 ? load_chunk(src[j] + s * BK, left) : u32x4{0u, 0u, 0u, 0u};
+    };
+    auto settle = [&](int buf) {   // registers to LDS
+        u32x4* dst = reinterpret_cast<u32x4*>(tile_lds + buf * kRows * BK) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[(j * 4 + wave) * 64] = reg[j];
+    };
+    f32x4 acc[RB][MB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int wn = wave & 1, wm = wave >> 1;
+    if (S > 0) {
+        fetch(0);
+        settle(0);
+    }
+    for (int s = 0; s < S; ++s) {
+        __syncthreads();   // step s is in LDS; everyone is done with the other buffer
+        if (s + 1 < S) fetch(s + 1);
+        const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + (s & 1) * kRows * BK) + r * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = (4 * h + g) ^ (r & 7);
             u32x4 fw[RB], fx[MB];
 #pragma unroll
-            for (int j = 0; j < MB; ++j) fx[j] = xl[j * 128 + pos[h]];
+            for (int j = 0; j < MB; ++j) fx[j] = base[(64 + (wm * MB + j) * 16) * 8 + pos];
 #pragma unroll
-            for (int i = 0; i < RB; ++i) fw[i] = wl[i * 128 + pos[h]];
+            for (int i = 0; i < RB; ++i) fw[i] = base[(wn * RB + i) * 128 + pos];
 #pragma unroll
             for (int i = 0; i < RB; ++i)
 #pragma unroll
                 for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
         }
-    };
-    if (S > 0) {
-        fetch(0, 0);
-        settle(0);
-    }
-    for (int s = 0; s < S; ++s) {
-        __syncthreads();   // step s is in LDS; everyone is done with the other buffer
-        if (s + 1 < S) fetch(s + 1, (s + 1) & 1);
-        compute(s & 1);
         if (s + 1 < S) settle((s + 1) & 1);
     }
-    __syncthreads();   // every wave is done with the tile buffers
-    static_assert(kWaves * out_stage_floats<RB>() * 4 <= 2 * kRows * BK * 2, "the sums fit the tile buffers");
+    __syncthreads();   // every wave is done with the buffers
     put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
                           n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
-}
-
-template <class T, int BM, int BN, int WM, int WN, bool GLU, bool DIRECT>
-hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
-    constexpr int kOutN = GLU ? BN / 2 : BN;
-    const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
-    const unsigned grid = (unsigned)((tiles + 7) / 8 * 8);
-    auto kernel = linear_tile_kernel<T, BM, BN, WM, WN, GLU, DIRECT>;
-    const size_t lds = (size_t)2 * (BN + BM) * BK * 2;
-    kernel<<<grid, 64 * WM * WN, lds, s>>>(a);
-    return hipGetLastError();
 }
 
 template <class T, int RB, int MB, int D, bool GLU>
@@ -825,18 +865,28 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
         if (mb == 2 || b32 <= 256) return launch_stream<T, 2, 2, 2, GLU>(a, w, s);
         return launch_stream<T, 2, 4, 2, GLU>(a, w, s);
     }
-    if (!a.aligned) return launch_tile<T, 64, 64, 2, 2, GLU, false>(a, s);
     const int64_t cols = GLU ? 2ll * a.N : a.N;
     auto tiles = [&](int64_t bn, int64_t bm) { return (cols + bn - 1) / bn * ((a.M + bm - 1) / bm); };
-    const int64_t t84 = tiles(256, 256);
-    if (t84 >= 128) {
-        const int64_t r84 = (t84 + 255) / 256 * 256, r64 = (tiles(192, 256) + 255) / 256 * 200;
-        if (r64 < r84) return launch_phased<T, 6, 4, GLU>(a, s);
-        return launch_phased<T, 8, 4, GLU>(a, s);
+    if (!a.aligned) {
+        linear_any_kernel<T, GLU><<<(unsigned)((tiles(64, 64) + 7) / 8 * 8), 256, 2 * 128 * BK * 2, s>>>(a);
+        return hipGetLastError();
     }
-    const int64_t mid = (int64_t)((a.N + (GLU ? 63 : 127)) / (GLU ? 64 : 128)) * ((a.M + 127) / 128);
-    if (mid >= 128) return launch_tile<T, 128, 128, 2, 2, GLU, true>(a, s);
-    return launch_tile<T, 64, 64, 2, 2, GLU, true>(a, s);
+    // The tile whose rounds (one workgroup per CU; two of the 64 x 64 tile)
+    // take least, by a full round's time for K = 4096, measured in us: small
+    // tiles fill the GPU, large ones read less per product. 256 x 4096 rows:
+    // 21 us with 64 x 64 tiles, 34 with 128 x 128; 1024 x 4096: 55, 39 and 55
+    // with 256 x 128; 2048 x 4096: 80, 67 and 85 with 256 x 256; 4096 x 4096:
+    // 127 with 256 x 128, 102 with 256 x 256.
+    auto rounds = [&](int64_t bn, int64_t bm, int64_t at_once) { return (tiles(bn, bm) + at_once - 1) / at_once; };
+    const int64_t cost[5] = {rounds(64, 64, 256) == 1 ? 21 : 28 * rounds(64, 64, 512), 39 * rounds(128, 128, 256),
+                             66 * rounds(128, 256, 256), 80 * rounds(192, 256, 256), 100 * rounds(256, 256, 256)};
+    switch (std::min_element(cost, cost + 5) - cost) {
+        case 0: return launch_ring<T, 64, 64, 2, 2, 4, GLU>(a, s);
+        case 1: return launch_ring<T, 128, 128, 2, 4, 4, GLU>(a, s);
+        case 2: return launch_ring<T, 256, 128, 4, 2, 3, GLU>(a, s);
+        case 3: return launch_phased<T, 6, 4, GLU>(a, s);
+        default: return launch_phased<T, 8, 4, GLU>(a, s);
+    }
 }
 
 }  // namespace
