@@ -160,26 +160,45 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _here(name: str, *tensors):
-    """The calls below launch on the current device: every tensor lives there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{cur}")
+def _here():
+    """(device index, raw handle of its current stream). The calls below
+    launch there; every tensor has to live on that device."""
+    dev = torch.cuda.current_device()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
+    return dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _rows(t: torch.Tensor, dtypes, shape, name: str):
-    """Pointer and row distance (in elements) of a 2-d device tensor whose
-    rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+def _on_gpu(t, dev: int, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _whole(t, dtype, shape, dev: int, name: str) -> int:
+    """Pointer of a contiguous tensor of the given type and shape."""
+    _on_gpu(t, dev, name)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dtypes, shape, dev: int, name: str):
+    """Pointer and row distance (in elements) of a 2-d tensor with
+    contiguous rows."""
+    _on_gpu(t, dev, name)
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 2 or tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), ld
 
 
 def _other_stream(stream):
@@ -217,26 +236,30 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
     if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be 2-d tensors")
-    (M, K), rows = x.shape, w.shape[0]
+    M, K = x.shape
+    rows = w.shape[0]
     if act == "swiglu" and rows % 2:
         raise ValueError("swiglu: w must have as many gate as up rows")
     N = rows // 2 if act == "swiglu" else rows
-    xp, ldx = _rows(x, (torch.bfloat16, torch.float16), (M, K), "x")
-    wp, ldw = _rows(w, (x.dtype,), (rows, K), "w")
+    _on_gpu(x, x.get_device(), "x")
+    dev, raw = _here()
+    xp, ldx = _rows(x, (torch.bfloat16, torch.float16), (M, K), dev, "x")
+    wp, ldw = _rows(w, (x.dtype,), (rows, K), dev, "w")
     if out_dtype is None:
         out_dtype = y.dtype if y is not None else (residual.dtype if residual is not None else x.dtype)
     if out_dtype not in _DTYPES:
         raise ValueError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
-    if bias is not None and tuple(bias.shape) != (rows,):
-        raise ValueError(f"bias must be [{rows}]")
-    bp = None if bias is None else _dev(bias, torch.float32, "bias")
-    rp, ldr = (None, N) if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
+    bp = None if bias is None else _whole(bias, torch.float32, (rows,), dev, "bias")
+    rp, ldr = (None, N) if residual is None else _rows(residual, (out_dtype,), (M, N), dev, "residual")
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    yp, ldy = _rows(y, (out_dtype,), (M, N), "y")
-    _here("linear", x, w, bias, residual, y)
+        yp, ldy = y.data_ptr(), N
+    else:
+        yp, ldy = _rows(y, (out_dtype,), (M, N), dev, "y")
     desc = LinearDesc(M, N, K, _DTYPES[x.dtype], _DTYPES[out_dtype], ACTIVATIONS[act], ldx, ldw, ldr, ldy)
-    _check(lib().pw_linear(ctypes.byref(desc), xp, wp, bp, rp, yp, _stream()))
+    status = lib().pw_linear(ctypes.byref(desc), xp, wp, bp, rp, yp, raw)
+    if status:
+        _check(status)
     return y
 
 
@@ -493,24 +516,25 @@ class PagedMoELayer:
             raise ValueError("score must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
         if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
             raise ValueError("logits must be [T, E]")
-        T = logits.shape[0]
-        lp, ld = _rows(logits, _DTYPES, (T, self.E), "logits")
-        if bias is not None and tuple(bias.shape) != (self.E,):
-            raise ValueError(f"bias must be [{self.E}]")
-        bp = None if bias is None else _dev(bias, torch.float32, "bias")
+        _on_gpu(logits, logits.get_device(), "logits")
+        T, E, k = logits.shape[0], self.E, self.k
+        dev, raw = _here()
+        lp, ld = _rows(logits, _DTYPES, (T, E), dev, "logits")
+        bp = None if bias is None else _whole(bias, torch.float32, (E,), dev, "bias")
         mp = None
         if mask is not None:
-            if tuple(mask.shape) != (T,) or mask.dtype not in (torch.bool, torch.uint8):
+            if mask.dtype not in (torch.bool, torch.uint8):
                 raise ValueError(f"mask must be bool or uint8 [{T}]")
-            mp = _dev(mask, mask.dtype, "mask")
-        _here("route_gated", logits, bias, mask)
-        ids = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
-        g = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
-        counts = torch.empty((self.E,), dtype=torch.int32, device=logits.device) if with_counts else None
-        desc = GateDesc(SCORES[score], n_group, topk_group, GROUP_SCORES[group_score], int(bool(renorm)), scale)
-        _check(lib().pw_route_gated(self._ctx, ctypes.byref(desc), lp, _DTYPES[logits.dtype], ld, bp, mp, T,
-                                    ids.data_ptr(), g.data_ptr(), None if counts is None else counts.data_ptr(),
-                                    _stream()), self._ctx)
+            mp = _whole(mask, mask.dtype, (T,), dev, "mask")
+        where = logits.device
+        ids = torch.empty((T, k), dtype=torch.int32, device=where)
+        g = torch.empty((T, k), dtype=torch.float32, device=where)
+        counts = torch.empty((E,), dtype=torch.int32, device=where) if with_counts else None
+        desc = GateDesc(SCORES[score], n_group, topk_group, GROUP_SCORES[group_score], 1 if renorm else 0, scale)
+        status = lib().pw_route_gated(self._ctx, ctypes.byref(desc), lp, _DTYPES[logits.dtype], ld, bp, mp, T,
+                                      ids.data_ptr(), g.data_ptr(), None if counts is None else counts.data_ptr(), raw)
+        if status:
+            _check(status, self._ctx)
         return ids, g, counts
 
     def moe_forward_routed(self, x: torch.Tensor, ids: torch.Tensor, g: torch.Tensor,
@@ -524,23 +548,27 @@ class PagedMoELayer:
         if side is not None:
             return _call_on(side, (x, ids, g, residual, y),
                             lambda: self.moe_forward_routed(x, ids, g, residual, y, out_dtype))
-        T = x.shape[0]
-        if x.dim() != 2 or x.shape[1] != self.d or tuple(ids.shape) != (T, self.k) or tuple(g.shape) != (T, self.k):
+        if x.dim() != 2 or x.shape[1] != self.d or ids.shape != (x.shape[0], self.k) or g.shape != ids.shape:
             raise ValueError("x must be [T, d], ids and g [T, k]")
         if out_dtype is None:
             out_dtype = y.dtype if y is not None else (residual.dtype if residual is not None else torch.float32)
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-        for t, n in ((residual, "residual"), (y, "y")):
-            if t is not None and tuple(t.shape) != (T, self.d):
-                raise ValueError(f"{n} must be [T, d]")
+        _on_gpu(x, x.get_device(), "x")
+        T = x.shape[0]
+        dev, raw = _here()
+        xp = _whole(x, torch.bfloat16, (T, self.d), dev, "x")
+        ip = _whole(ids, torch.int32, (T, self.k), dev, "ids")
+        gp = _whole(g, torch.float32, (T, self.k), dev, "g")
+        rp = None if residual is None else _whole(residual, out_dtype, (T, self.d), dev, "residual")
         if y is None:
             y = torch.empty((T, self.d), dtype=out_dtype, device=x.device)
-        _here("moe_forward_routed", x, ids, g, residual, y)
-        _check(lib().pw_moe_forward_routed(self._ctx, _dev(x, torch.bfloat16, "x"), _dev(ids, torch.int32, "ids"),
-                                           _dev(g, torch.float32, "g"), T,
-                                           None if residual is None else _dev(residual, out_dtype, "residual"),
-                                           _dev(y, out_dtype, "y"), _DTYPES[out_dtype], _stream()), self._ctx)
+            yp = y.data_ptr()
+        else:
+            yp = _whole(y, out_dtype, (T, self.d), dev, "y")
+        status = lib().pw_moe_forward_routed(self._ctx, xp, ip, gp, T, rp, yp, _DTYPES[out_dtype], raw)
+        if status:
+            _check(status, self._ctx)
         return y
 
     def moe_block(self, x: torch.Tensor, gate_w: torch.Tensor, gate_logit_bias: Optional[torch.Tensor] = None,
