@@ -12,13 +12,14 @@
 //
 // The choice is that of the exact scores. Where c is the logit (no bias, and
 // groups by their largest) it is exact as it stands. Otherwise c is taken in
-// fp32, every comparison that decides something is checked against a bound
-// on its error, and a token with a nearer pair is chosen again from scores
-// in fp64 (about 1 token in 500 at 256 experts).
+// fp64 with a short exponential (about 2^-36 of a score; 20 instructions per
+// expert), every comparison that decides something is checked against a
+// bound on its error, and a token with a nearer pair is chosen again from
+// full fp64 scores. (With fp32 scores and the same check one token in a
+// thousand had to be: its wave took 10 us longer, and with it the launch.)
 //
-// Keys: c as a double has 29 free mantissa bits (fp32) and takes the expert
-// id in its low 10, so one v_max_f64 orders (c, lower id first) exactly. The
-// fp64 scores are compared whole, the ids apart from them.
+// Keys: c as a double with the expert id in its low 10 bits (a converted
+// fp32 logit leaves 29 empty), so one v_max_f64 orders (c, lower id first).
 //
 // A token is routed by L lanes of a wave, lane l holding experts l, l + L,
 // ...: 16 lanes (four tokens a wave, reductions inside a DPP row) for
@@ -43,9 +44,13 @@ constexpr int kGateBlock = 256;
 constexpr double kGone = -0x1p300;      // key of an expert that is not to be had
 constexpr double kGoneBelow = -0x1p250; // keys below: none left
 constexpr double kMost = 0x1p200;       // key of c = +inf (above every fp32 value)
-// relative error bounds of the fp32 scores: a score has at most 20 2^-24 of
-// the largest score in it and the sum with the bias rounds by 2^-24 |c|
-constexpr double kTol = 0x1p-19;
+// How far two choice scores can be from their exact difference, as a
+// multiple of (|c| + S), S = 1 (sigmoid) or the largest score (softmax): the
+// exponential is off by at most 2^-36 of itself (exp_short), so a score by
+// 2^-35 of S, and a key by the 10 bits the id takes, 2^-42 |c|; for two 2^-34
+// S + 2^-41 |c|, twice that for sums of two scores (taken with 2 S and the
+// sum of their |c|).
+constexpr double kTol = 0x1p-33;
 
 __device__ __forceinline__ double max_f64(double a, double b) {
     double d;
@@ -99,21 +104,55 @@ __device__ __forceinline__ float lanes_fmax(float x) {
     return x;
 }
 
-// c and the expert id as one key
-__device__ __forceinline__ double make_key(double c, int e) {
-    if (!(c > kGoneBelow)) return kGone;   // -inf and NaN
-    c = c == 0.0 ? 0.0 : (c > kMost ? kMost : c);
-    uint64_t u = __builtin_bit_cast(uint64_t, c) & ~1023ull;
-    u |= (uint64_t)((u >> 63) ? e : 1023 - e);
-    return __builtin_bit_cast(double, u);
+// c (fp32, -inf: not to be had) and the expert id as one key: the id, its
+// bits turned for positive c so that lower ids are larger either way, in the
+// low bits that a converted fp32 number leaves empty
+__device__ __forceinline__ double make_key(float c, int e) {
+    const double d = max_f64(min_f64((double)(c + 0.0f), kMost), kGone);   // -0 as +0
+    const uint64_t u = __builtin_bit_cast(uint64_t, d);
+    const int neg = (int)(u >> 32) >> 31;
+    const uint32_t lo = (uint32_t)u | (uint32_t)((neg & 1023) ^ (e ^ 1023));
+    return __builtin_bit_cast(double, (u & 0xffffffff00000000ull) | lo);
 }
 __device__ __forceinline__ int key_id(double k) {
     const uint64_t u = __builtin_bit_cast(uint64_t, k);
     const int i = (int)(u & 1023u);
     return (u >> 63) ? i : 1023 - i;
 }
-__device__ __forceinline__ double key_c(double k) {
-    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull);
+
+// The same for fp64 scores (their low 10 bits go).
+__device__ __forceinline__ double make_key(double c, int e) {
+    const double d = max_f64(min_f64(c + 0.0, kMost), kGone);   // -inf and NaN: kGone
+    const uint64_t u = __builtin_bit_cast(uint64_t, d);
+    const int neg = (int)(u >> 32) >> 31;
+    const uint32_t lo = ((uint32_t)u & ~1023u) | (uint32_t)((neg & 1023) ^ (e ^ 1023));
+    return __builtin_bit_cast(double, (u & 0xffffffff00000000ull) | lo);
+}
+
+// e^x for x <= 0 in fp64: x = n ln 2 + r, |r| <= 0.3466, the Taylor polynomial
+// of degree 9 (remainder r^10 / 10! < 2^-37) and 2^n; r is off by n ln2 2^-53
+// and the sums by a few 2^-53, so the whole by less than 2^-36.
+__device__ __forceinline__ double exp_short(double x) {
+    x = max_f64(x, -800.0);
+    const double n = rint(x * 1.4426950408889634);
+    const double r = fma(-n, 0.69314718055994531, x);
+    double p = 1.0 / 362880.0;
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+// 1 / d for 1 <= d <= 2048: the instruction's estimate and one Newton step
+// (an estimate good to 2^-20 already gives 2^-40)
+__device__ __forceinline__ double rcp_short(double d) {
+    const double y = __builtin_amdgcn_rcp(d);
+    return fma(y, fma(-d, y, 1.0), y);
 }
 
 // e^x for x <= 0 with the rounding of x log2(e) carried along: within 3
@@ -144,19 +183,20 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The groups that stay, as a bit mask (G <= 64), of experts scored c[i]
-// (kGone: not to be had), approximately (near is set where the
-// scores do not decide) or exactly. c goes through the token's LDS row (E
-// doubles), the groups' scores through gs_row (2 G doubles).
-template <int L, int PER, class CF>
-__device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, CF c, double* row, double* gs_row, bool approx,
-                                                double top_s, bool& near) {
+// The groups that stay, as a bit mask (G <= 64), of experts scored c[i] (below
+// kGoneBelow: not to be had; scores or keys, whose id bits order equal groups
+// like their numbers); tol > 0: the scores are approximate, near is set
+// where they do not decide. c goes through the token's LDS row (E doubles),
+// the groups' scores through gs_row (2 G doubles).
+template <int L, int PER>
+__device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, const double (&c)[PER], double* row, double* gs_row,
+                                                double tol, double top_s, bool& near) {
     const int l = threadIdx.x & (L - 1);
     const int G = a.n_group, gs = a.E / G;
     wave_fence();   // the row's former readers are done
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        if (l + L * i < a.E) row[l + L * i] = c(i);
+        if (l + L * i < a.E) row[l + L * i] = c[i];
     wave_fence();
     // p lanes per group, the largest power of two that lets all groups go at
     // once (one lane, and several rounds, if there are more groups than lanes)
@@ -168,9 +208,11 @@ __device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, CF c, double*
             // each group starts at another place: groups of 32 experts
             // would otherwise read one LDS bank
             int at = sub + q % gs;
+            const double* src = row + q * gs;
+#pragma unroll 4
             for (int i = sub; i < gs; i += p) {
-                if (at >= gs) at -= gs;
-                const double v = row[q * gs + at];
+                at = at >= gs ? at - gs : at;
+                const double v = src[at];
                 m2 = max_f64(m2, min_f64(m1, v));
                 m1 = max_f64(m1, v);
                 at += p;
@@ -217,11 +259,11 @@ __device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, CF c, double*
         const uint64_t mine_bits = L == 64 ? b : (b >> ((threadIdx.x & 63) & ~(L - 1))) & 0xffffull;
         kept |= mine_bits << q0;
     }
-    if (approx) {
+    if (tol > 0.0) {
         low_kept = -lanes_max<L>(-low_kept);
         high_out = lanes_max<L>(high_out);
         size = lanes_max<L>(size);
-        if (high_out > kGoneBelow && low_kept - high_out <= kTol * (size + 2.0 * top_s)) near = true;
+        if (high_out > kGoneBelow && low_kept - high_out <= tol * (size + 2.0 * top_s)) near = true;
     }
     return kept;
 }
@@ -229,13 +271,13 @@ __device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, CF c, double*
 // The k largest keys: lane l gets choice l in id0 and, with 16 lanes, choice
 // l + 16 in id1 (-1: none). near as above.
 template <int L, int PER>
-__device__ __forceinline__ void choose(const GateArgs& a, double (&key)[PER], bool approx, double top_s, int& id0,
+__device__ __forceinline__ void choose(const GateArgs& a, double (&key)[PER], double tol, double top_s, int& id0,
                                        int& id1, bool& near) {
     const int l = threadIdx.x & (L - 1);
     id0 = id1 = -1;
     double prev = kMost * 4.0;
     for (int j = 0;; ++j) {
-        if (j == a.k && !approx) break;
+        if (j == a.k && tol == 0.0) break;
         double m[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) m[i] = key[i];
@@ -245,7 +287,7 @@ __device__ __forceinline__ void choose(const GateArgs& a, double (&key)[PER], bo
             for (int i = 0; i + h < PER; i += 2 * h) m[i] = max_f64(m[i], m[i + h]);
         const double best = lanes_max<L>(m[0]);
         const bool any = best > kGoneBelow;
-        if (approx && any && prev - best <= kTol * (fabs(best) + top_s)) near = true;
+        if (tol > 0.0 && any && prev - best <= tol * (fabs(best) + top_s)) near = true;
         if (j == a.k) break;
         prev = best;
         const int e = any ? key_id(best) : -1;
@@ -311,40 +353,60 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
 #pragma unroll
         for (int i = 1; i < PER; ++i) m = fmaxf(m, v[i]);
         m = lanes_fmax<L>(m);
+    }
+    if (softmax && by_logit && !a.renorm) {
         den = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) den += v[i] == -INFINITY ? 0.0f : (v[i] == m ? 1.0f : exp_neg(v[i] - m));
         den = lanes_sum<L>(den);
     }
-    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-    // fp32 score of a logit
-    auto score32 = [&](float x) {
-        if (softmax) return (x == m ? 1.0f : exp_neg(x - m)) * inv;
-        const float ex = exp_neg(-fabsf(x));
-        return (x < 0.0f ? ex : 1.0f) / (1.0f + ex);
-    };
-    double key[PER];
+    double key[PER], top_s = 1.0;
+    if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = l + L * i;
-        float c = v[i];
-        if (!by_logit && c > -INFINITY) c = score32(c) + (a.bias ? a.bias[e] : 0.0f);
-        key[i] = make_key((double)c, e);
+        for (int i = 0; i < PER; ++i) key[i] = make_key(v[i], l + L * i);
+    } else {
+        double inv = 1.0;
+        if (softmax) {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                key[i] = v[i] == -INFINITY ? 0.0 : (v[i] == m ? 1.0 : exp_short((double)v[i] - (double)m));
+                sum += key[i];
+            }
+            sum = lanes_sum<L>(sum);
+            den = (float)sum;
+            inv = top_s = sum > 0.0 ? rcp_short(sum) : 0.0;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = l + L * i;
+            double sc;
+            if (softmax) {
+                sc = key[i] * inv;
+            } else {
+                const double ex = exp_short(-fabs((double)v[i]));
+                sc = (v[i] < 0.0f ? ex : 1.0) * rcp_short(1.0 + ex);
+            }
+            if (a.bias && e < a.E) sc += (double)a.bias[e];
+            key[i] = make_key(v[i] > -INFINITY && sc == sc ? sc : -INFINITY, e);
+        }
     }
-    const double top_s = softmax ? (double)inv : 1.0;
-    auto drop_groups = [&](uint64_t kept, double (&key)[PER]) {
+    bool near = false;
+    int id0, id1;
+    if (a.n_group > 1) {
+        const uint64_t kept = keep_groups<L, PER>(a, key, row, gs_row, by_logit ? 0.0 : kTol, top_s, near);
+        // without a bias the logits give the order within the groups that stay
+        if (!by_logit && !a.bias) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) key[i] = make_key(v[i], l + L * i);
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int q = (int)(((uint32_t)(l + L * i) * a.group_magic) >> 20);
             if (!((kept >> (q & 63)) & 1)) key[i] = kGone;
         }
-    };
-    bool near = false;
-    int id0, id1;
-    if (a.n_group > 1)
-        drop_groups(keep_groups<L, PER>(a, [&](int i) { return key_c(key[i]); }, row, gs_row, !by_logit, top_s, near),
-                    key);
-    choose<L, PER>(a, key, !by_logit, top_s, id0, id1, near);
+    }
+    choose<L, PER>(a, key, a.bias ? kTol : 0.0, top_s, id0, id1, near);
     if (!by_logit && __any(near)) {
         // scores in fp64 (the whole wave; tokens that were decided keep
         // their choice)
@@ -356,23 +418,32 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
                 den64 += v[i] == -INFINITY ? 0.0 : (v[i] == m ? 1.0 : exp((double)v[i] - (double)m));
             den64 = lanes_sum<L>(den64);
         }
+        double s64[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = l + L * i;
-            double c = -INFINITY;
+            double sc = kGone;
             if (v[i] > -INFINITY) {
                 const double x = (double)v[i];
-                if (softmax) c = (v[i] == m ? 1.0 : exp(x - (double)m)) / den64;
-                else c = 1.0 / (1.0 + exp(-x));
-                if (a.bias) c += (double)a.bias[e];
+                if (softmax) sc = (v[i] == m ? 1.0 : exp(x - (double)m)) / den64;
+                else sc = 1.0 / (1.0 + exp(-x));
+                if (a.bias) sc += (double)a.bias[e];
+                sc = max_f64(min_f64(sc, kMost), kGone);
             }
-            key[i] = c > kGoneBelow ? (c > kMost ? kMost : c) : kGone;
+            s64[i] = sc;
         }
         bool none = false;
         int i0, i1;
-        if (a.n_group > 1)
-            drop_groups(keep_groups<L, PER>(a, [&](int i) { return key[i]; }, row, gs_row, false, top_s, none), key);
-        choose_exact<L, PER>(a, key, i0, i1);
+        if (a.n_group > 1) {
+            const uint64_t kept = keep_groups<L, PER>(a, s64, row, gs_row, 0.0, top_s, none);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int q = (int)(((uint32_t)(l + L * i) * a.group_magic) >> 20);
+                if (!a.bias) s64[i] = v[i] > -INFINITY ? min_f64((double)v[i], kMost) : kGone;
+                if (!((kept >> (q & 63)) & 1)) s64[i] = kGone;
+            }
+        }
+        choose_exact<L, PER>(a, s64, i0, i1);
         if (near) {
             id0 = i0;
             id1 = i1;
@@ -407,30 +478,26 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
     if (L == 16) put(l + 16, id1, w1);
 }
 
-// ONE: the whole batch in one workgroup of 1024 threads, which also counts
+// ONE: the whole batch in one workgroup, a wave per token, which also counts
 // the pairs of each expert in LDS; else a token per L lanes over the grid
 // (workgroup 0 clears the counts for the kernel that follows).
 template <int L, int PER, class TL, bool ONE>
 __global__ __launch_bounds__(ONE ? 1024 : kGateBlock) void gate_kernel(GateArgs a) {
     extern __shared__ __attribute__((aligned(16))) double gate_lds[];
     __shared__ int hist[ONE ? kMaxExperts : 1];
-    constexpr int kTokens = (ONE ? 1024 : kGateBlock) / L;
     const int slot = threadIdx.x / L;
     double* row = gate_lds + (int64_t)slot * (a.E + 2 * a.n_group);
     if constexpr (ONE) {
-        for (int e = threadIdx.x; e < a.E; e += 1024) hist[e] = 0;
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
-        for (int t0 = 0; t0 < a.T; t0 += kTokens) {
-            const int t = t0 + slot;
-            gate_token<L, PER, TL>(a, t < a.T ? t : 0, t < a.T, row, row + a.E, a.counts ? hist : nullptr);
-        }
+        gate_token<L, PER, TL>(a, slot, true, row, row + a.E, a.counts ? hist : nullptr);
         __syncthreads();
         if (a.counts)
-            for (int e = threadIdx.x; e < a.E; e += 1024) a.counts[e] = hist[e];
+            for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = hist[e];
     } else {
         if (a.counts && blockIdx.x == 0)
             for (int e = threadIdx.x; e < a.E; e += kGateBlock) a.counts[e] = 0;
-        const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
+        const int64_t t = (int64_t)blockIdx.x * (kGateBlock / L) + slot;
         gate_token<L, PER, TL>(a, t < a.T ? (int)t : 0, t < a.T, row, row + a.E, nullptr);
     }
 }
@@ -441,9 +508,14 @@ __global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* ids, in
     __shared__ int hist[kMaxExperts];
     for (int e = threadIdx.x; e < E; e += 1024) hist[e] = 0;
     __syncthreads();
-    for (int64_t p = (int64_t)blockIdx.x * 1024 + threadIdx.x; p < P; p += (int64_t)gridDim.x * 1024) {
-        const int e = ids[p];
-        if (e >= 0) atomicAdd(&hist[e], 1);
+    const int64_t step = (int64_t)gridDim.x * 1024;
+    for (int64_t p0 = (int64_t)blockIdx.x * 1024 + threadIdx.x; p0 < P; p0 += 8 * step) {
+        int e[8];   // their loads together
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = p0 + i * step < P ? ids[p0 + i * step] : -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e[i] >= 0) atomicAdd(&hist[e[i]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 1024)
@@ -461,8 +533,8 @@ hipError_t launch_gate_t(const GateArgs& a0, hipStream_t s) {
     a.group_lanes = 1;
     while (2 * a.group_lanes * a.n_group <= L) a.group_lanes *= 2;
     const size_t row = a.n_group > 1 ? ((size_t)a.E + 2 * a.n_group) * sizeof(double) : 0;
-    if (L == 64 && a.T <= kOneTokens && row * 16 <= 64 * 1024) {
-        gate_kernel<64, (L == 64 ? PER : 1), TL, true><<<1, 1024, row * 16, s>>>(a);
+    if (L == 64 && a.T <= kOneTokens && row * a.T <= 64 * 1024) {
+        gate_kernel<64, (L == 64 ? PER : 1), TL, true><<<1, 64 * a.T, row * a.T, s>>>(a);
         return hipGetLastError();
     }
     const int per = kGateBlock / L;
