@@ -39,6 +39,7 @@ struct pw_ctx {
     uint64_t ws_bytes = 0;
     int dg_parity = 0;    // counter set of the streaming kernels' grouping used by the next forward
     bool dg_clean = false;   // both counter sets cleared since the workspace was bound
+    bool rg_clean = false;   // the counter set of given routes is clear
 
     // host tier: with pinned host memory bound, the pages live there and the
     // pool is a cache of page slots (residency state on the device)
@@ -686,6 +687,7 @@ pw_status pw_bind_workspace(pw_ctx* c, void* ws, uint64_t bytes) {
     c->ws_bytes = bytes;
     c->dg_parity = 0;
     c->dg_clean = false;   // cleared by the first streaming forward's stream
+    c->rg_clean = false;
     return PW_OK;
 }
 
@@ -838,8 +840,19 @@ struct GivenRoutes {
 };
 
 // Given routes into the scratch, grouped for the path of the batch. The
-// counter set of these calls is cleared at each of them, so that neither a
-// replayed graph nor a forward between replays finds another's counts.
+// counter set is these calls' own, cleared once after binding the workspace
+// (and after a call that failed on its way) and left clear by each of them,
+// in stream order. A call under capture runs when its graph is replayed, so
+// it says nothing about the set now, and clears it itself.
+static bool capturing(hipStream_t s) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &st) != hipSuccess) {
+        (void)hipGetLastError();
+        return true;
+    }
+    return st != hipStreamCaptureStatusNone;
+}
+
 static pw_status accept_batch(pw_ctx* c, const WsView& v, const FwdWork& w, const GivenRoutes& r, const void* x,
                               int32_t T, bool dense, hipStream_t s, KTimer t, const int32_t** counts, int own_route) {
     RouteArgs ra{nullptr, static_cast<const uint16_t*>(x), c->d, T, c->E, c->k, c->desc.renorm, 1,
@@ -853,8 +866,10 @@ static pw_status accept_batch(pw_ctx* c, const WsView& v, const FwdWork& w, cons
         return PW_OK;
     }
     ra.group = own_route ? 0 : 1;
-    if (ra.group)
+    const bool later = capturing(s);
+    if (ra.group && (later || !c->rg_clean))
         HIP_TRY(c, launch_zero_i32(reinterpret_cast<int32_t*>(v.base + v.lay.rg), v.lay.dg_bytes / 8, s));
+    if (!later) c->rg_clean = false;   // until the combine is enqueued
     HIP_TRY(c, launch_accept_routes(ra, w, r.ids, r.g, s, t));
     *counts = w.dg.cnt;
     return PW_OK;
@@ -982,6 +997,7 @@ static pw_status forward_core(pw_ctx* c, const WsView& v, const void* x, const f
         HIP_TRY(c, launch_down(fa, plan_ffn(c->F, T, nsplit), s, tm[2]));
         HIP_TRY(c, combine(nsplit));
     }
+    if (given && !dense && !capturing(s)) c->rg_clean = true;   // by the combine
     if (c->profile_mask && !scratch) c->forwards_timed++;
     return PW_OK;
 }

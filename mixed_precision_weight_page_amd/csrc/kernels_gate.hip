@@ -246,6 +246,7 @@ __device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, const double 
         if (q < G) {
             const double mine = gs_row[q];
             int rank = 0;
+#pragma unroll 8
             for (int j = 0; j < G; ++j) {
                 const double v = gs_row[j];
                 rank += (v > mine || (v == mine && j < q)) ? 1 : 0;
@@ -343,6 +344,16 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
         v[i] = (live && e < a.E) ? to_f32(src[e]) : -INFINITY;
         if (!(v[i] > lowest_of<TL>())) v[i] = -INFINITY;   // NaN too
     }
+    // with 64 lanes (few tokens) the bias is loaded with the logits; 16 lanes
+    // load it where it is used (its registers would cost a wave per SIMD:
+    // 16384 x 256 took 28 us instead of 23)
+    auto bias_of = [&](int i) { return a.bias && l + L * i < a.E ? a.bias[l + L * i] : 0.0f; };
+    float b[L == 64 ? PER : 1];
+    if constexpr (L == 64) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) b[i] = bias_of(i);
+    }
+    auto bias = [&](int i) { return (double)(L == 64 ? b[L == 64 ? i : 0] : bias_of(i)); };
     const bool softmax = a.score == PW_SCORE_SOFTMAX;
     const bool by_logit = !a.bias && !(a.n_group > 1 && a.group_top2);
     // softmax: the largest logit and the sum of the exponentials, where the
@@ -387,7 +398,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
                 const double ex = exp_short(-fabs((double)v[i]));
                 sc = (v[i] < 0.0f ? ex : 1.0) * rcp_short(1.0 + ex);
             }
-            if (a.bias && e < a.E) sc += (double)a.bias[e];
+            sc += bias(i);
             key[i] = make_key(v[i] > -INFINITY && sc == sc ? sc : -INFINITY, e);
         }
     }
@@ -421,13 +432,12 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
         double s64[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = l + L * i;
             double sc = kGone;
             if (v[i] > -INFINITY) {
                 const double x = (double)v[i];
                 if (softmax) sc = (v[i] == m ? 1.0 : exp(x - (double)m)) / den64;
                 else sc = 1.0 / (1.0 + exp(-x));
-                if (a.bias) sc += (double)a.bias[e];
+                sc += bias(i);
                 sc = max_f64(min_f64(sc, kMost), kGone);
             }
             s64[i] = sc;
@@ -478,11 +488,13 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
     if (L == 16) put(l + 16, id1, w1);
 }
 
-// ONE: the whole batch in one workgroup, a wave per token, which also counts
+// ONE: the whole batch in one workgroup, L lanes per token, which also counts
 // the pairs of each expert in LDS; else a token per L lanes over the grid
 // (workgroup 0 clears the counts for the kernel that follows).
+constexpr int one_threads(int per) { return per > 8 ? 512 : 1024; }   // what their registers allow
+
 template <int L, int PER, class TL, bool ONE>
-__global__ __launch_bounds__(ONE ? 1024 : kGateBlock) void gate_kernel(GateArgs a) {
+__global__ __launch_bounds__(ONE ? one_threads(PER) : kGateBlock) void gate_kernel(GateArgs a) {
     extern __shared__ __attribute__((aligned(16))) double gate_lds[];
     __shared__ int hist[ONE ? kMaxExperts : 1];
     const int slot = threadIdx.x / L;
@@ -490,7 +502,7 @@ __global__ __launch_bounds__(ONE ? 1024 : kGateBlock) void gate_kernel(GateArgs 
     if constexpr (ONE) {
         for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
-        gate_token<L, PER, TL>(a, slot, true, row, row + a.E, a.counts ? hist : nullptr);
+        gate_token<L, PER, TL>(a, slot < a.T ? slot : 0, slot < a.T, row, row + a.E, a.counts ? hist : nullptr);
         __syncthreads();
         if (a.counts)
             for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = hist[e];
@@ -522,8 +534,6 @@ __global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* ids, in
         if (hist[e]) atomicAdd(&counts[e], hist[e]);
 }
 
-// One workgroup up to this many tokens: its 16 waves take one token each.
-constexpr int kOneTokens = 16;
 // 64 lanes per token up to this many tokens (they spread over the GPU)
 constexpr int kWaveTokens = 1024;
 
@@ -533,8 +543,9 @@ hipError_t launch_gate_t(const GateArgs& a0, hipStream_t s) {
     a.group_lanes = 1;
     while (2 * a.group_lanes * a.n_group <= L) a.group_lanes *= 2;
     const size_t row = a.n_group > 1 ? ((size_t)a.E + 2 * a.n_group) * sizeof(double) : 0;
-    if (L == 64 && a.T <= kOneTokens && row * a.T <= 64 * 1024) {
-        gate_kernel<64, (L == 64 ? PER : 1), TL, true><<<1, 64 * a.T, row * a.T, s>>>(a);
+    const int64_t threads = ((int64_t)a.T * L + 63) / 64 * 64;
+    if (threads <= one_threads(PER) && (size_t)(threads / L) * row <= 64 * 1024) {
+        gate_kernel<L, PER, TL, true><<<1, (unsigned)threads, row * (size_t)(threads / L), s>>>(a);
         return hipGetLastError();
     }
     const int per = kGateBlock / L;
@@ -549,7 +560,10 @@ hipError_t launch_gate_t(const GateArgs& a0, hipStream_t s) {
 
 template <class TL>
 hipError_t launch_gate_d(const GateArgs& a, hipStream_t s) {
-    if (a.E > 256 || a.T <= kWaveTokens) {
+    // one workgroup up to 64 tokens if 16 lanes can take one (to 16 at 64
+    // lanes each)
+    const bool rows = a.E <= 256 && (a.T > kWaveTokens || (a.counts && a.T > 16 && a.T <= (a.E <= 128 ? 64 : 32)));
+    if (!rows) {
         const int per = (a.E + 63) / 64;
         if (per == 1) return launch_gate_t<64, 1, TL>(a, s);
         if (per == 2) return launch_gate_t<64, 2, TL>(a, s);

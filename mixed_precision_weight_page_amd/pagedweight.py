@@ -252,7 +252,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     bp = None if bias is None else _whole(bias, torch.float32, (rows,), dev, "bias")
     rp, ldr = (None, N) if residual is None else _rows(residual, (out_dtype,), (M, N), dev, "residual")
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = x.new_empty((M, N), dtype=out_dtype)
         yp, ldy = y.data_ptr(), N
     else:
         yp, ldy = _rows(y, (out_dtype,), (M, N), dev, "y")
@@ -526,10 +526,9 @@ class PagedMoELayer:
             if mask.dtype not in (torch.bool, torch.uint8):
                 raise ValueError(f"mask must be bool or uint8 [{T}]")
             mp = _whole(mask, mask.dtype, (T,), dev, "mask")
-        where = logits.device
-        ids = torch.empty((T, k), dtype=torch.int32, device=where)
-        g = torch.empty((T, k), dtype=torch.float32, device=where)
-        counts = torch.empty((E,), dtype=torch.int32, device=where) if with_counts else None
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+        g = logits.new_empty((T, k), dtype=torch.float32)
+        counts = logits.new_empty((E,), dtype=torch.int32) if with_counts else None
         desc = GateDesc(SCORES[score], n_group, topk_group, GROUP_SCORES[group_score], 1 if renorm else 0, scale)
         status = lib().pw_route_gated(self._ctx, ctypes.byref(desc), lp, _DTYPES[logits.dtype], ld, bp, mp, T,
                                       ids.data_ptr(), g.data_ptr(), None if counts is None else counts.data_ptr(), raw)

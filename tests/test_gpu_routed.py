@@ -194,6 +194,29 @@ def test_captured_routed_forward_replays(name, shape, T, layout):
         assert torch.equal(got, eager), i
 
 
+def test_a_graph_captured_first_and_not_replayed():
+    """A capture before any other call leaves nothing behind: the eager call
+    after it, the graph's replay after that, and calls between replays with
+    other batch sizes all count from zero."""
+    wl, layer, experts = build("capture_first", dict(E=32, d=256, F=384, k=2), 40, "eq2")
+    x, _ = synth.tokens(wl, T=40)
+    xd = x.cuda()
+    ids, g = routes(40, wl.E, wl.k, 1)
+    i, w = ids.cuda(), g.cuda()
+    torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(0x7f)
+    layer.bind_workspace(torch.full((layer.workspace_bytes(),), 0x7f, dtype=torch.uint8, device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.moe_forward_routed(xd, i, w)
+    want = reference(x, ids, g, None, experts)
+    compare(layer.moe_forward_routed(xd, i, w), want, "eager after the capture")
+    for n in (40, 17, 3):
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(y, want, "replay")
+        compare(layer.moe_forward_routed(xd[:n], i[:n], w[:n]), reference(x[:n], ids[:n], g[:n], None, experts), f"eager {n}")
+
+
 def test_given_routes_with_a_host_tier():
     wl, layer, experts = build("tier", dict(E=16, d=256, F=384, k=2), 40, "eq2")
     x, _ = synth.tokens(wl, T=40)
