@@ -177,6 +177,13 @@ __device__ __forceinline__ void copy_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, 
 #endif
 }
 
+// 4 bytes per lane, likewise (64 of them at dst).
+__device__ __forceinline__ void touch_to_lds(const __amdgpu_buffer_rsrc_t& rsrc, uint16_t* dst, uint32_t off, int soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 4, (int)off, soff, 0, 0);
+#endif
+}
+
 // byte offset of K value k0, 0 past the end (the lanes are out of bounds there)
 __device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 : 0; }
 
@@ -527,9 +534,17 @@ __device__ __forceinline__ bool tile_of(int tn, int tm, int& nt, int& mt) {
 // others read). Copies past the last stage read zeros (out of the buffer's
 // bounds).
 //
+// A layer's weights come from memory each time it runs, 1 to 2 us away where
+// a stage takes 1: each of the 8 token tiles that share a weight tile on an
+// XCD asks for an eighth of its rows kAhead stages ahead (four bytes of each
+// 128-byte row part, into LDS that nobody reads), which brings them into the
+// L2 (8192 x 4096 x 4096 from memory: 255 -> 238 us; the tokens too: 231, but
+// 3% slower where they were written just before).
+//
 // A row's 16-byte chunk c lies at position c ^ (row % 8): the rows of an
 // operand read fall on different banks (no conflicts counted; 64-byte rows
 // had one cycle in three).
+constexpr int kAhead = 4;
 template <class T, int RB, int MB, bool GLU>
 __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
     constexpr int BN = 32 * RB, BM = 64 * MB, kRows = BN + BM;
@@ -572,6 +587,19 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
         for (int j = 0; j < QW + QX; ++j)
             copy_to_lds(j < QW ? rw : rx, dst + 64 * j * BK, in ? off[j] : kOutside, in_bytes(k0, a.K));
     };
+    // the row this lane asks for early, if any: four of a wave, which lie in
+    // one block of 16 and so are of one kind with SwiGLU
+    const int lr0 = (mt & 7) * (BN / 8) + 4 * wave;
+    uint32_t ahead = kOutside;
+    if (lane < 4 && 4 * wave < BN / 8) {
+        const int lr = lr0 + lane;
+        const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
+        if (n0 + wr < a.N) ahead = (uint32_t)(wr * a.ldw) * 2u;
+    }
+    const auto ra = make_rsrc(wbase + (GLU && ((lr0 >> 4) & 1) ? (int64_t)a.N * a.ldw : 0));
+    auto touch = [&](int s) {
+        touch_to_lds(ra, tile_lds + 2 * kRows * BK + wave * 128, s * BK < a.K ? ahead : kOutside, in_bytes(s * BK, a.K));
+    };
     f32x4 acc[RB][MB];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -581,7 +609,10 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
     const bool late = wave >= 4;
     const int S = (a.K + BK - 1) / BK;
     copy(0);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int s = 1; s < kAhead; ++s) touch(s);
+    // the copies are older than the touches
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kAhead - 1) : "memory");
     if (late) asm volatile("s_barrier" ::: "memory");
     for (int s = 0; s < S; ++s) {
 #pragma unroll
@@ -594,11 +625,14 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
 #pragma unroll
             for (int i = 0; i < RB; ++i) fw[i] = base[(wn * RB + i) * 128];
             __builtin_amdgcn_sched_barrier(0);
-            if (h == 1 && late) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (h == 1 && late) asm volatile("s_waitcnt vmcnt(1)" ::: "memory");   // all but the last touch
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_setprio(1);
-            if (h == 0) copy(s + 1);
+            if (h == 0) {
+                copy(s + 1);
+                touch(s + kAhead);   // the last: the waits below count on it
+            }
 #pragma unroll
             for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -606,14 +640,14 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
             if (h == 0) {
                 // a copy after every second matrix instruction
 #pragma unroll
-                for (int q = 0; q < QW + QX; ++q) {
+                for (int q = 0; q < QW + QX + 1; ++q) {
                     __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
                     __builtin_amdgcn_sched_group_barrier(0x10, 1, 0);
                 }
             }
             __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
-            if (h == 1 && !late) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (h == 1 && !late) asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
             asm volatile("s_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -633,7 +667,7 @@ hipError_t launch_phased(const LinearArgs& a, hipStream_t s) {
     constexpr int kOutN = GLU ? 16 * RB : 32 * RB, BM = 64 * MB;
     const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
     linear_phased_kernel<T, RB, MB, GLU>
-        <<<(unsigned)((tiles + 7) / 8 * 8), 512, (size_t)2 * (32 * RB + BM) * BK * 2, s>>>(a);
+        <<<(unsigned)((tiles + 7) / 8 * 8), 512, (size_t)2 * (32 * RB + BM) * BK * 2 + 8 * 256, s>>>(a);
     return hipGetLastError();
 }
 
