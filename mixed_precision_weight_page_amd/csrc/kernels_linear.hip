@@ -225,8 +225,9 @@ __device__ __forceinline__ void join_waves(const LinearArgs& a, const f32x4 (&ac
 // of gate and of up rows), MB blocks of 16 tokens, the K range dealt to its
 // waves in pieces of 64: neighbouring waves read neighbouring 128 bytes of
 // every row, straight into MFMA operands, D pieces in flight per wave. The
-// waves' sums meet in LDS. Weights are read once: non-temporal loads keep
-// the tokens in the caches.
+// waves' sums meet in LDS. (A lane's K values are 32 contiguous bytes, so that
+// its two loads come from one 128-byte line: 50 us for 16 x 14336 x 4096
+// SwiGLU, 62 with 64-byte halves of the lines and non-temporal loads.)
 template <class T, int RB, int MB, int D, bool GLU>
 __global__ __launch_bounds__(RB * MB > 4 ? 256 : 1024) void linear_skinny_kernel(LinearArgs a) {
     extern __shared__ __attribute__((aligned(16))) float part[];   // [waves][RB][MB][64 lanes][4]
@@ -477,18 +478,21 @@ __device__ __forceinline__ void put_tile_t(const LinearArgs& a, const f32x4 (&ac
 #pragma unroll
             for (int t = 0; t < kIter; ++t) store_quad<DT>(a.y, at + (int64_t)(t * kStep) * a.ldy, v[t]);
         } else {
+            // ragged or unaligned: value by value, the residual's loads
+            // together
+            float add[kIter][4];
 #pragma unroll
-            for (int t = 0; t < kIter; ++t) {
-                const int64_t m = m1 + t * kStep;
-                if (m >= a.M) break;
+            for (int t = 0; t < kIter; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (n + e >= a.N) break;
-                    float o = v[t][e];
-                    if (a.residual) o += load_out(a.residual, m * a.ldr + n + e, DT);
-                    store_out(a.y, m * a.ldy + n + e, DT, o);
-                }
-            }
+                for (int e = 0; e < 4; ++e)
+                    add[t][e] = a.residual && m1 + t * kStep < a.M && n + e < a.N
+                                    ? load_out(a.residual, (m1 + t * kStep) * a.ldr + n + e, DT) : 0.0f;
+#pragma unroll
+            for (int t = 0; t < kIter; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m1 + t * kStep < a.M && n + e < a.N)
+                        store_out(a.y, (m1 + t * kStep) * a.ldy + n + e, DT, a.residual ? v[t][e] + add[t][e] : v[t][e]);
         }
     }
 }
@@ -768,12 +772,14 @@ hipError_t launch_ring(const LinearArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Rows of any alignment: 64 weight rows x 64 tokens, 2 x 2 waves, K in steps
-// of 64 through two LDS buffers; the rows go through registers, loaded a step
-// ahead with unaligned loads. LDS layout as above.
+// Rows of any alignment: 64 weight rows x 64 tokens, WN x WM waves, K in
+// steps of 64 through two LDS buffers; the rows go through registers, loaded
+// two steps ahead with unaligned loads. LDS layout as above.
+constexpr int kAnyWN = 2, kAnyWM = 4;
 template <class T, bool GLU>
-__global__ __launch_bounds__(256) void linear_any_kernel(LinearArgs a) {
-    constexpr int RB = 2, MB = 2, kRows = 128;
+__global__ __launch_bounds__(64 * kAnyWN * kAnyWM) void linear_any_kernel(LinearArgs a) {
+    constexpr int kWaves = kAnyWN * kAnyWM, kRows = 128;
+    constexpr int RB = 4 / kAnyWN, MB = 4 / kAnyWM, Q = kRows / 8 / kWaves;
     constexpr int kOutN = GLU ? 32 : 64;
     extern __shared__ __attribute__((aligned(16))) uint16_t tile_lds[];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -783,47 +789,43 @@ __global__ __launch_bounds__(256) void linear_any_kernel(LinearArgs a) {
     if (!tile_of((a.N + kOutN - 1) / kOutN, (a.M + 63) / 64, nt, mt)) return;
     const int n0 = nt * kOutN;
     const int64_t m0 = (int64_t)mt * 64;
-    // this thread's chunks: LDS rows 32 j + 8 wave + lane / 8 (j < 2 weights,
-    // then tokens), position lane % 8
+    // this thread's chunks: LDS rows 8 (kWaves j + wave) + lane / 8 (64 of the
+    // weights, then the tokens), position lane % 8
     const int crow = lane >> 3, chunk = (lane & 7) ^ crow;
-    const uint16_t* src[4];
+    const uint16_t* src[Q];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int lr = 32 * (j & 1) + 8 * wave + crow;
-        if (j < 2) {
+    for (int j = 0; j < Q; ++j) {
+        const int lr = 8 * (kWaves * j + wave) + crow, xr = lr - 64;
+        if (lr < 64) {
             const int wr = GLU ? (lr >> 5) * 16 + (lr & 15) : lr;
             const int64_t row = (GLU && ((lr >> 4) & 1) ? (int64_t)a.N : 0) + n0 + wr;
             src[j] = n0 + wr < a.N ? reinterpret_cast<const uint16_t*>(a.w) + row * a.ldw + 8 * chunk : nullptr;
         } else {
-            src[j] = m0 + lr < a.M ? reinterpret_cast<const uint16_t*>(a.x) + (m0 + lr) * a.ldx + 8 * chunk : nullptr;
+            src[j] = m0 + xr < a.M ? reinterpret_cast<const uint16_t*>(a.x) + (m0 + xr) * a.ldx + 8 * chunk : nullptr;
         }
     }
     const int S = (a.K + BK - 1) / BK;
-    u32x4 reg[4];
-    auto fetch = [&](int s) {
+    u32x4 even[Q], odd[Q];   // the rows of an even and of an odd step
+    auto fetch = [&](int s, u32x4 (&reg)[Q]) {
         const int left = a.K - (s * BK + 8 * chunk);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < Q; ++j)
             reg[j] = src[j] && left > 0 ? load_chunk(src[j] + s * BK, left) : u32x4{0u, 0u, 0u, 0u};
     };
-    auto settle = [&](int buf) {   // registers to LDS
-        u32x4* dst = reinterpret_cast<u32x4*>(tile_lds + buf * kRows * BK) + lane;
+    auto settle = [&](int s, const u32x4 (&reg)[Q]) {   // registers to LDS
+        u32x4* dst = reinterpret_cast<u32x4*>(tile_lds + (s & 1) * kRows * BK) + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dst[(j * 4 + wave) * 64] = reg[j];
+        for (int j = 0; j < Q; ++j) dst[(kWaves * j + wave) * 64] = reg[j];
     };
     f32x4 acc[RB][MB];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int wn = wave & 1, wm = wave >> 1;
-    if (S > 0) {
-        fetch(0);
-        settle(0);
-    }
-    for (int s = 0; s < S; ++s) {
+    const int wn = wave % kAnyWN, wm = wave / kAnyWN;
+    auto step = [&](int s, u32x4 (&mine)[Q], const u32x4 (&other)[Q]) {
         __syncthreads();   // step s is in LDS; everyone is done with the other buffer
-        if (s + 1 < S) fetch(s + 1);
+        if (s + 2 < S) fetch(s + 2, mine);
         const u32x4* base = reinterpret_cast<const u32x4*>(tile_lds + (s & 1) * kRows * BK) + r * 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -838,9 +840,19 @@ __global__ __launch_bounds__(256) void linear_any_kernel(LinearArgs a) {
 #pragma unroll
                 for (int j = 0; j < MB; ++j) acc[i][j] = mma<T>(fw[i], fx[j], acc[i][j]);
         }
-        if (s + 1 < S) settle((s + 1) & 1);
+        if (s + 1 < S) settle(s + 1, other);
+    };
+    if (S > 0) {
+        fetch(0, even);
+        if (S > 1) fetch(1, odd);
+        settle(0, even);
+    }
+    for (int s = 0; s < S; s += 2) {
+        step(s, even, odd);
+        if (s + 1 < S) step(s + 1, odd, even);
     }
     __syncthreads();   // every wave is done with the buffers
+    static_assert(kWaves * out_stage_floats<RB>() * 4 <= 2 * kRows * BK * 2, "the sums fit the buffers");
     put_tile<RB, MB, GLU>(a, acc, reinterpret_cast<float*>(tile_lds) + wave * out_stage_floats<RB>(),
                           n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
 }
@@ -902,7 +914,8 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     const int64_t cols = GLU ? 2ll * a.N : a.N;
     auto tiles = [&](int64_t bn, int64_t bm) { return (cols + bn - 1) / bn * ((a.M + bm - 1) / bm); };
     if (!a.aligned) {
-        linear_any_kernel<T, GLU><<<(unsigned)((tiles(64, 64) + 7) / 8 * 8), 256, 2 * 128 * BK * 2, s>>>(a);
+        linear_any_kernel<T, GLU>
+            <<<(unsigned)((tiles(64, 64) + 7) / 8 * 8), 64 * kAnyWN * kAnyWM, 2 * 128 * BK * 2, s>>>(a);
         return hipGetLastError();
     }
     // The tile whose rounds (one workgroup per CU; two of the 64 x 64 tile)

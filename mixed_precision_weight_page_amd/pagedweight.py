@@ -160,19 +160,27 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _here():
-    """(device index, raw handle of its current stream). The calls below
-    launch there; every tensor has to live on that device."""
-    dev = torch.cuda.current_device()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
-    return dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+# handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _on_gpu(t, dev: int, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
+
+
+def _here(t, name: str):
+    """(device index, raw handle of its current stream) of a call on t. The
+    library launches on the current device, so t has to live there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev, _raw_stream(dev)
 
 
 def _whole(t, dtype, shape, dev: int, name: str) -> int:
@@ -241,8 +249,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     if act == "swiglu" and rows % 2:
         raise ValueError("swiglu: w must have as many gate as up rows")
     N = rows // 2 if act == "swiglu" else rows
-    _on_gpu(x, x.get_device(), "x")
-    dev, raw = _here()
+    dev, raw = _here(x, "x")
     xp, ldx = _rows(x, (torch.bfloat16, torch.float16), (M, K), dev, "x")
     wp, ldw = _rows(w, (x.dtype,), (rows, K), dev, "w")
     if out_dtype is None:
@@ -516,9 +523,8 @@ class PagedMoELayer:
             raise ValueError("score must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
         if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
             raise ValueError("logits must be [T, E]")
-        _on_gpu(logits, logits.get_device(), "logits")
         T, E, k = logits.shape[0], self.E, self.k
-        dev, raw = _here()
+        dev, raw = _here(logits, "logits")
         lp, ld = _rows(logits, _DTYPES, (T, E), dev, "logits")
         bp = None if bias is None else _whole(bias, torch.float32, (E,), dev, "bias")
         mp = None
@@ -553,9 +559,8 @@ class PagedMoELayer:
             out_dtype = y.dtype if y is not None else (residual.dtype if residual is not None else torch.float32)
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-        _on_gpu(x, x.get_device(), "x")
         T = x.shape[0]
-        dev, raw = _here()
+        dev, raw = _here(x, "x")
         xp = _whole(x, torch.bfloat16, (T, self.d), dev, "x")
         ip = _whole(ids, torch.int32, (T, self.k), dev, "ids")
         gp = _whole(g, torch.float32, (T, self.k), dev, "g")
