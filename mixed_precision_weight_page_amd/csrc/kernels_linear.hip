@@ -3,9 +3,11 @@
 // then the N up rows. bf16 or fp16 operands, fp32 accumulation on the matrix
 // cores, everything after the product in fp32, one rounding to y's type.
 //
-// Up to kSkinnyTokens tokens the weights' bytes bound it: linear_skinny_kernel
-// streams them from memory straight into MFMA operands. Beyond,
-// linear_tile_kernel multiplies LDS tiles.
+// Up to kSkinnyTokens tokens the weights' bytes bound it: they are streamed
+// once, straight into MFMA operands (linear_skinny_kernel) or through each
+// wave's own LDS ring (linear_stream_kernel). Beyond, tiles of both operands
+// meet in LDS: linear_phased_kernel (large products), linear_ring_kernel
+// (smaller ones), linear_any_kernel (rows of any alignment).
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -884,7 +886,7 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
         const int64_t b32 = ((GLU ? 2ll * a.N : a.N) + 31) / 32;   // blocks of 32 weight rows
         auto waves_for = [&](int64_t blocks) {
             int w = 4;
-            while (w < 16 && blocks * w < 3072 && w * BK < a.K) w *= 2;
+            while (w < 16 && blocks * w < 3000 && w * BK < a.K) w *= 2;
             return w;
         };
         // few rows: a workgroup per 16 of them and per 16 tokens, up to 16
