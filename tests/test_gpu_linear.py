@@ -145,6 +145,19 @@ def test_phased_stages(K):
     run(2305, 1990, K, "swiglu", "f16", "f16", residual=True)
 
 
+# a size for each of the five tiles (64 x 64, 128 x 128, 128 rows x 256
+# tokens, 192 x 256, 256 x 256), ragged, with fewer and more steps of K than
+# its LDS holds
+TILES = [(200, 300), (1100, 2300), (2100, 2900), (4000, 2800), (4000, 3900)]
+
+
+@pytest.mark.parametrize("K", [0, 8, 64, 72, 200, 392])
+@pytest.mark.parametrize("M,N", TILES)
+def test_every_tile(M, N, K):
+    run(M, N, K, "none", "bf16", "bf16", bias=True, residual=True)
+    run(M, N // 2, K, "swiglu", "f16", "f32", residual=True, pads=(8, 16, 4, 4))
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 512, 8192), (1, 256, 14336), (512, 256, 8192)])
 def test_long_sums(M, N, K):
     run(M, N, K, "none", "bf16", "f32")
