@@ -122,7 +122,7 @@ __device__ __forceinline__ int key_id(double k) {
 
 // The same for fp64 scores (their low 10 bits go).
 __device__ __forceinline__ double make_key(double c, int e) {
-    const double d = max_f64(min_f64(c + 0.0, kMost), kGone);   // -inf and NaN: kGone
+    const double d = max_f64(min_f64(c + 0.0, kMost), kGone);   // -inf: kGone (c is not NaN)
     const uint64_t u = __builtin_bit_cast(uint64_t, d);
     const int neg = (int)(u >> 32) >> 31;
     const uint32_t lo = ((uint32_t)u & ~1023u) | (uint32_t)((neg & 1023) ^ (e ^ 1023));
@@ -445,7 +445,8 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
                 if (softmax) sc = (v[i] == m ? 1.0 : exp(x - (double)m)) / den64;
                 else sc = 1.0 / (1.0 + exp(-x));
                 sc += bias(i);
-                sc = max_f64(min_f64(sc, kMost), kGone);
+                // a NaN c is not chosen (v_min_f64 would make it kMost)
+                sc = sc == sc ? max_f64(min_f64(sc, kMost), kGone) : kGone;
             }
             s64[i] = sc;
         }

@@ -1,0 +1,64 @@
+"""GPU tests of pw_route_gated's choice bias where it is no ordinary number
+(NaN, -inf, +inf) and scores tie, so that the choice is made again from fp64
+scores. Logits take a few values only: choice scores are equal or far apart,
+so the oracle's ids and counts have to be met exactly; weights as in
+test_gpu_gate.py (logits within 32 of each other)."""
+import math
+
+import pytest
+import torch
+
+from layer_cases import log
+from oracle import gate as gate_oracle
+
+pytestmark = pytest.mark.gpu
+
+LOW = float(torch.finfo(torch.float32).min)
+WTOL = 2.0 ** -19
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def check(layer, logits, **kw):
+    """logits and tensors of kw on the CPU; kw as route_gated's."""
+    dev = {n: (v.cuda() if isinstance(v, torch.Tensor) else v) for n, v in kw.items()}
+    ids, g, counts = layer.route_gated(logits.cuda(), **dev)
+    opt = dict(kw, bias=None if kw.get("bias") is None else kw["bias"].double().tolist())
+    opt["top2"] = opt.pop("group_score", "max") == "top2"
+    want_ids, want_g, want_counts = gate_oracle.route(logits.double().tolist(), LOW, layer.k, **opt)
+    want = torch.tensor(want_ids, dtype=torch.int32)
+    off = (ids.cpu() != want).any(dim=1)
+    assert not bool(off.any()), (int(off.nonzero()[0]), ids[off.cuda()][0].tolist(), want[off][0].tolist(), kw)
+    wg = torch.tensor(want_g, dtype=torch.float64)
+    assert bool(((g.cpu().double() - wg).abs() <= WTOL * wg.abs()).all())
+    assert counts.cpu().tolist() == want_counts
+
+
+def tied(T, E, seed):
+    """Logits 0, 1 and 2 in random places: sums of two scores too are equal or
+    differ by a twentieth of themselves."""
+    return torch.randint(0, 3, (T, E), generator=torch.Generator().manual_seed(seed)).float()
+
+
+# one token per 64 lanes in one workgroup and in several, per 16 lanes in one
+# and in several
+@pytest.mark.parametrize("T", [1, 16, 30, 70, 1100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_bias_of_nan_among_equal_scores(T, score):
+    from mixed_precision_weight_page_amd import PagedMoELayer
+    for E, k in ((4, 2), (24, 6), (64, 8)):
+        layer = PagedMoELayer(E, 128, 128, k, max_tokens=T)
+        bias = torch.zeros(E)
+        bias[1] = math.nan
+        bias[E - 1] = -math.inf
+        log(f"NaN bias T={T} E={E} {score}")
+        for logits in (torch.zeros(T, E), tied(T, E, T + E)):
+            check(layer, logits, score=score, bias=bias)
+            check(layer, logits, score=score, bias=bias, n_group=2, topk_group=2, renorm=True)
+            if E > 4:
+                for by in ("max", "top2"):
+                    check(layer, logits, score=score, bias=bias, n_group=4, topk_group=2, group_score=by, renorm=True)
