@@ -235,7 +235,7 @@ __device__ __forceinline__ uint64_t keep_groups(const GateArgs& a, const double 
             score = m1;
             size = fabs(m1);
             if (a.group_top2 && m2 > kGoneBelow) {
-                score += m2;
+                score = min_f64(score + m2, kMost);   // inf + inf is not above inf
                 size += fabs(m2);
             }
         }

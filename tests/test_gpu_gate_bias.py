@@ -62,3 +62,20 @@ def test_a_bias_of_nan_among_equal_scores(T, score):
             if E > 4:
                 for by in ("max", "top2"):
                     check(layer, logits, score=score, bias=bias, n_group=4, topk_group=2, group_score=by, renorm=True)
+
+
+@pytest.mark.parametrize("T", [1, 16, 30, 70, 1100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_with_one_and_with_two_infinite_scores_are_equal(T, score):
+    """A group's sum is infinite with one c of +inf as with two: the lower
+    group stays."""
+    from mixed_precision_weight_page_amd import PagedMoELayer
+    for E, n_group, k, at in ((16, 4, 2, (1, 4, 5)), (64, 8, 5, (9, 16, 23, 63)), (256, 8, 8, (40, 64, 95, 255))):
+        layer = PagedMoELayer(E, 128, 128, k, max_tokens=T)
+        bias = torch.zeros(E)
+        bias[list(at)] = math.inf
+        log(f"infinite bias T={T} E={E} {score}")
+        for logits in (torch.zeros(T, E), tied(T, E, T + E)):
+            for topk_group in (1, 2):
+                for by in ("max", "top2"):
+                    check(layer, logits, score=score, bias=bias, n_group=n_group, topk_group=topk_group, group_score=by)
