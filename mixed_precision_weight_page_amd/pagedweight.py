@@ -210,11 +210,18 @@ def _rows(t, dtypes, shape, dev: int, name: str):
 
 
 def _other_stream(stream):
-    """None if `stream` is the current one (or None), else it as a torch stream."""
+    """None if `stream` is the current one (or None), else it as a torch
+    stream. An integer is a handle on the current device, 0 its default stream."""
     if stream is None:
         return None
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    return None if s.cuda_stream == torch.cuda.current_stream().cuda_stream else s
+    here = torch.cuda.current_stream()
+    if hasattr(stream, "cuda_stream"):
+        return None if (stream.cuda_stream, stream.device) == (here.cuda_stream, here.device) else stream
+    raw = int(stream)
+    if raw == here.cuda_stream:
+        return None
+    # ExternalStream takes a null handle for none given, and makes a new stream
+    return torch.cuda.default_stream() if raw == 0 else torch.cuda.ExternalStream(raw)
 
 
 def _call_on(stream, tensors, call):
