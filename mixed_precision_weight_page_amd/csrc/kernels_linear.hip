@@ -186,6 +186,10 @@ __device__ __forceinline__ void touch_to_lds(const __amdgpu_buffer_rsrc_t& rsrc,
 #endif
 }
 
+// Waits count copies in the order in which they were issued (s_waitcnt vmcnt):
+// where they tell older from younger ones, no memory access may change sides.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
 // byte offset of K value k0, 0 past the end (the lanes are out of bounds there)
 __device__ __forceinline__ int in_bytes(int k0, int K) { return k0 < K ? 2 * k0 : 0; }
 
@@ -360,7 +364,10 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearArgs a) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < D; ++j) copy(j, j);
+    for (int j = 0; j < D; ++j) {
+        copy(j, j);
+        keep_order();
+    }
     int slot = 0;
     for (int i = 0; i < n; ++i) {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (RB + MB) * (D - 1)) : "memory");
@@ -615,6 +622,7 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
     const bool late = wave >= 4;
     const int S = (a.K + BK - 1) / BK;
     copy(0);
+    keep_order();
 #pragma unroll
     for (int s = 1; s < kAhead; ++s) touch(s);
     // the copies are older than the touches
@@ -637,6 +645,7 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
             __builtin_amdgcn_s_setprio(1);
             if (h == 0) {
                 copy(s + 1);
+                keep_order();
                 touch(s + kAhead);   // the last: the waits below count on it
             }
 #pragma unroll
@@ -733,7 +742,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_ring_kernel(LinearArgs a)
     const int wn = wave % WN, wm = wave / WN;
     const int S = (a.K + BK - 1) / BK;
 #pragma unroll
-    for (int j = 0; j < D - 1; ++j) copy(j, j);
+    for (int j = 0; j < D - 1; ++j) {
+        copy(j, j);
+        keep_order();
+    }
     int slot = 0;
     for (int s = 0; s < S; ++s) {
         // step s is whole (this wave's part, then everyone's), and everyone
