@@ -1040,13 +1040,15 @@ pw_status pw_moe_forward_noalloc(pw_ctx* c, const void* x, const float* logits, 
     v.max_tokens = T;
     v.nsplit = (int64_t)T * c->k > 2048 ? 1 : down_splits(c->F, c->d, 1, 1 << 30);
     v.lay = workspace_layout(c->E, c->d, c->F, c->k, T, v.nsplit);
-    if (v.lay.total > noalloc_scratch_bytes()) {
+    // (the counters of given routes come last in the layout and are not used
+    // here: what has to fit ends where they start)
+    if (v.lay.rg > noalloc_scratch_bytes()) {
         v.nsplit = 1;
         v.lay = workspace_layout(c->E, c->d, c->F, c->k, T, 1);
     }
-    if (v.lay.total > noalloc_scratch_bytes())
+    if (v.lay.rg > noalloc_scratch_bytes())
         return fail(c, PW_ERR_WORKSPACE, "a forward of %d tokens needs %llu bytes of scratch, the static scratch "
-                    "holds %llu", T, (unsigned long long)v.lay.total,
+                    "holds %llu", T, (unsigned long long)v.lay.rg,
                     (unsigned long long)noalloc_scratch_bytes());
     void* p = nullptr;
     if (noalloc_scratch(c->device, &p) != hipSuccess || !p)

@@ -60,3 +60,31 @@ def test_noalloc_refuses_a_batch_larger_than_its_scratch():
     layer.moe_forward_noalloc(x.cuda(), logits.cuda(), y)
     torch.cuda.synchronize()
     compare_y(y, oracle_y(x, logits, wl, masters, wl.bits), "noalloc after a refused batch")
+
+
+def test_noalloc_takes_the_largest_batch_its_scratch_holds():
+    """The scratch a forward needs is the workspace without the two counter
+    sets of given routes (each cnt [E], act [E] and two more, in 256 bytes):
+    the last batch within the array runs, the next one is refused."""
+    from mixed_precision_weight_page_amd import PagedMoELayer, PagedWeightError
+    E, d, F, k, array = 1024, 128, 128, 1, 64 << 20
+    sets = 2 * ((4 * (2 * E + 2) + 255) // 256 * 256)
+    need = lambda T: PagedMoELayer(E, d, F, k, max_tokens=T).workspace_bytes() - sets  # noqa: E731
+    lo, hi = 1, 1 << 16
+    while lo < hi:   # the first batch that does not fit
+        mid = (lo + hi) // 2
+        lo, hi = (lo, mid) if need(mid) > array else (mid + 1, hi)
+    T = lo - 1
+    assert need(T) <= array < need(T) + sets
+    wl = synth.WORKLOADS["decode_fine"].scaled(name="noalloc_limit", E=E, d=d, F=F, k=k, T=T + 1)
+    layer, _ = make_layer(wl, synth.expert_weights(wl), max_tokens=T + 1)
+    layer.quantize_experts([(3, 4, 8)[e % 3] for e in range(E)])
+    x, logits = (t.cuda() for t in synth.tokens(wl, T=T + 1))
+    log(f"noalloc: largest batch, {T} tokens")
+    want = layer.moe_forward(x[:T], logits[:T])
+    y = torch.full((T, d), float("nan"), device="cuda")
+    layer.moe_forward_noalloc(x[:T], logits[:T], y)
+    torch.cuda.synchronize()
+    compare_y(y, want.cpu().double(), "largest batch")
+    with pytest.raises(PagedWeightError, match="scratch"):
+        layer.moe_forward_noalloc(x, logits, torch.empty((T + 1, d), device="cuda"))
