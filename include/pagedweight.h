@@ -16,7 +16,8 @@
  * Conventions (every entry point):
  *   - Returns pw_status: 0 on success, a negative code on error. Nothing
  *     aborts or throws. pw_last_error(ctx) gives a message for the last
- *     failed call on that context.
+ *     failed call on that context, pw_last_error(NULL) for the calling
+ *     thread's last failed pw_linear, which has none.
  *   - Device pointers are BORROWED: the caller (for example PyTorch) owns
  *     the memory and keeps it alive while the context uses it. Host
  *     pointers are read or written only during the call.

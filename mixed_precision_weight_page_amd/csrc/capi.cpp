@@ -84,16 +84,18 @@ namespace {
 constexpr size_t kAlign = 256;
 inline uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 
+// The calling thread's last failure of a call without a context (pw_linear).
+thread_local char g_err[512] = "null context";
+
 pw_status fail(pw_ctx* c, pw_status s, const char* fmt, ...) {
-    if (c) {
-        char buf[512];
-        va_list ap;
-        va_start(ap, fmt);
-        vsnprintf(buf, sizeof buf, fmt, ap);
-        va_end(ap);
-        c->err = buf;
-        if (getenv("PW_LOG")) fprintf(stderr, "[pagedweight] %s\n", buf);
-    }
+    char buf[sizeof g_err];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    if (c) c->err = buf;
+    else std::memcpy(g_err, buf, sizeof buf);
+    if (getenv("PW_LOG")) fprintf(stderr, "[pagedweight] %s\n", buf);
     return s;
 }
 
@@ -1134,11 +1136,14 @@ pw_status pw_route_gated(pw_ctx* c, const pw_gate_desc* gate, const void* logits
 
 pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
                     const void* residual, void* y, void* stream) {
-    if (!desc) return PW_ERR_INVALID_ARG;
+    auto bad = [](const char* fmt, auto... v) { return fail(nullptr, PW_ERR_INVALID_ARG, fmt, v...); };
+    if (!desc) return bad("%s", "null description");
     const pw_linear_desc& d = *desc;
-    if (d.M < 0 || d.N < 0 || d.K < 0 || d.N > (1 << 30) || d.K > (1 << 29)) return PW_ERR_INVALID_ARG;
-    if ((d.in_dtype != PW_BF16 && d.in_dtype != PW_F16) || !dtype_ok(d.out_dtype)) return PW_ERR_INVALID_ARG;
-    if (d.act < PW_ACT_NONE || d.act > PW_ACT_SWIGLU) return PW_ERR_INVALID_ARG;
+    if (d.M < 0 || d.N < 0 || d.K < 0 || d.N > (1 << 30) || d.K > (1 << 29))
+        return bad("M = %d, N = %d, K = %d: none may be negative, N at most 2^30, K 2^29", d.M, d.N, d.K);
+    if ((d.in_dtype != PW_BF16 && d.in_dtype != PW_F16) || !dtype_ok(d.out_dtype))
+        return bad("x and w must be bf16 or fp16 (got type %d), y fp32, fp16 or bf16 (got %d)", d.in_dtype, d.out_dtype);
+    if (d.act < PW_ACT_NONE || d.act > PW_ACT_SWIGLU) return bad("unknown activation %d", d.act);
     if (d.M == 0 || d.N == 0) return PW_OK;
     LinearArgs a{};
     const bool glu = d.act == PW_ACT_SWIGLU;
@@ -1149,12 +1154,19 @@ pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, co
     a.ldr = d.M > 1 ? d.ldr : d.N;
     a.ldy = d.M > 1 ? d.ldy : d.N;
     constexpr int64_t kMaxLd = (int64_t)1 << 22;   // 256 rows of a tile within a 31-bit byte offset
-    if (a.ldx < d.K || a.ldw < d.K || a.ldy < d.N || (residual && a.ldr < d.N)) return PW_ERR_INVALID_ARG;
-    if ((d.M > 1 && a.ldx >= kMaxLd) || (rows > 1 && a.ldw >= kMaxLd)) return PW_ERR_INVALID_ARG;
-    if (!y || (d.K > 0 && (!x || !w))) return PW_ERR_INVALID_ARG;
+    auto row_bad = [&](const char* name, int64_t ld, int32_t cols) {
+        return bad("rows of %s are %lld elements apart, each has %d", name, (long long)ld, cols);
+    };
+    if (a.ldx < d.K) return row_bad("x", a.ldx, d.K);
+    if (a.ldw < d.K) return row_bad("w", a.ldw, d.K);
+    if (a.ldy < d.N) return row_bad("y", a.ldy, d.N);
+    if (residual && a.ldr < d.N) return row_bad("residual", a.ldr, d.N);
+    if ((d.M > 1 && a.ldx >= kMaxLd) || (rows > 1 && a.ldw >= kMaxLd))
+        return bad("rows of x are %lld and of w %lld elements apart: must be below 2^22", (long long)a.ldx, (long long)a.ldw);
+    if (!y || (d.K > 0 && (!x || !w))) return bad("null %s", !y ? "y" : !x ? "x" : "w");
     const uintptr_t ob = elem_bytes(d.out_dtype);
     if ((uintptr_t)x % 2 || (uintptr_t)w % 2 || (uintptr_t)bias % 4 || (uintptr_t)residual % ob || (uintptr_t)y % ob)
-        return PW_ERR_INVALID_ARG;
+        return bad("%s", "a pointer is not aligned to its elements");
     a.x = x;
     a.w = w;
     a.bias = bias;
@@ -1169,7 +1181,8 @@ pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, co
     a.aligned = (uintptr_t)x % 16 == 0 && (uintptr_t)w % 16 == 0 && d.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0;
     a.vec_out = (uintptr_t)y % (4 * ob) == 0 && (d.M == 1 || a.ldy % 4 == 0) &&
                 (!residual || ((uintptr_t)residual % (4 * ob) == 0 && (d.M == 1 || a.ldr % 4 == 0)));
-    return launch_linear(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PW_OK : PW_ERR_HIP;
+    const hipError_t e = launch_linear(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? PW_OK : fail(nullptr, PW_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
 }
 
 pw_status pw_get_page_table(const pw_ctx* c, pw_page_entry* out) {
@@ -1219,6 +1232,6 @@ pw_status pw_profile_read(pw_ctx* c, pw_profile_data* out) {
     return PW_OK;
 }
 
-const char* pw_last_error(const pw_ctx* c) { return c ? c->err.c_str() : "null context"; }
+const char* pw_last_error(const pw_ctx* c) { return c ? c->err.c_str() : g_err; }
 
 }  // extern "C"

@@ -273,7 +273,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     desc = LinearDesc(M, N, K, _DTYPES[x.dtype], _DTYPES[out_dtype], ACTIVATIONS[act], ldx, ldw, ldr, ldy)
     status = lib().pw_linear(ctypes.byref(desc), xp, wp, bp, rp, yp, raw)
     if status:
-        _check(status)
+        raise PagedWeightError(status, lib().pw_last_error(None).decode())
     return y
 
 

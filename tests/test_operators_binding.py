@@ -1,5 +1,10 @@
 """Host-only checks of the Python binding of the calls around the expert
 layer. No call here touches a GPU."""
+import ctypes
+import os
+import threading
+
+import pytest
 import torch
 
 from mixed_precision_weight_page_amd import pagedweight as pwb
@@ -38,3 +43,42 @@ def test_which_stream_a_call_runs_on(monkeypatch):
     here[0] = default
     other = Stream(0, device=1)
     assert pwb._other_stream(other) is other
+
+
+needs_lib = pytest.mark.skipif(not os.path.exists(pwb.library_path()), reason="library not built")
+FAKE, ODD = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 1)
+
+
+def c_linear(x=FAKE, w=FAKE, r=None, y=FAKE, desc=True, **kw):
+    """pw_linear on pointers that a refused call never reads."""
+    d = pwb.LinearDesc(**{**dict(M=4, N=8, K=16, in_dtype=2, out_dtype=2, act=0, ldx=16, ldw=16, ldr=8, ldy=8), **kw})
+    return pwb.lib().pw_linear(ctypes.byref(d) if desc else None, x, w, None, r, y, None)
+
+
+@needs_lib
+def test_every_refusal_of_linear_says_why():
+    L = pwb.lib()
+    for bad, word in ((dict(desc=False), b"description"), (dict(M=-1), b"M = -1"), (dict(K=(1 << 29) + 1), b"2^29"),
+                      (dict(in_dtype=0), b"type 0"), (dict(out_dtype=3), b"got 3"), (dict(act=7), b"activation 7"),
+                      (dict(ldx=15), b"rows of x are 15"), (dict(ldw=15), b"rows of w are 15"), (dict(ldy=7), b"rows of y are 7"),
+                      (dict(r=FAKE, ldr=7), b"rows of residual are 7"), (dict(ldx=1 << 22), b"2^22"), (dict(x=None), b"null x"),
+                      (dict(w=None), b"null w"), (dict(y=None), b"null y"), (dict(x=ODD), b"aligned")):
+        assert c_linear(**bad) == -1, bad
+        assert word in L.pw_last_error(None), (bad, L.pw_last_error(None))
+    # the message is the calling thread's own
+    other = []
+    t = threading.Thread(target=lambda: other.extend([c_linear(act=9), L.pw_last_error(None)]))
+    t.start()
+    t.join()
+    assert other[0] == -1 and b"activation 9" in other[1]
+    assert b"aligned" in L.pw_last_error(None)
+
+
+@needs_lib
+def test_the_binding_passes_the_reason_on(monkeypatch):
+    # everything up to the library's own checks, as if the tensors were on a GPU
+    monkeypatch.setattr(pwb, "_here", lambda t, name: (0, None))
+    monkeypatch.setattr(pwb, "_on_gpu", lambda t, dev, name: None)
+    x, w = torch.zeros(1, 16, dtype=torch.bfloat16).expand(4, 16), torch.zeros(8, 16, dtype=torch.bfloat16)
+    with pytest.raises(pwb.PagedWeightError, match="rows of x are 0 elements apart"):
+        pwb.linear(x, w)
