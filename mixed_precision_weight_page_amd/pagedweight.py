@@ -166,6 +166,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 
 def _on_gpu(t, dev: int, name: str):
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient and this call is forward only: detach it, or call under torch.no_grad()")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.get_device() != dev:
@@ -243,7 +245,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     act "swiglu" [2 N, K]: gate rows, then up rows) bf16 or fp16, bias fp32,
     residual and y [M, N] of out_dtype (default: y's, residual's or x's
     type); rows may be strided. act: none, relu, silu, sigmoid, gelu,
-    gelu_tanh, swiglu. residual may be y."""
+    gelu_tanh, swiglu. residual may be y. Forward only, as the layer's calls
+    below: tensors that require a gradient are refused where one is recorded."""
     side = _other_stream(stream)
     if side is not None:
         return _call_on(side, (x, w, bias, residual, y), lambda: linear(x, w, bias, act, residual, y, out_dtype))

@@ -61,3 +61,22 @@ def test_stream_zero_is_the_default_stream(monkeypatch):
     for got, w in zip(outs[2], want[1:]):
         assert torch.equal(got, w)
     assert torch.equal(outs[3], b.layer.moe_forward_routed(x, want[1], want[2]))
+
+
+def test_tensors_that_require_a_gradient():
+    """Refused one by one where gradients are recorded; under no_grad the
+    same tensors give the same block."""
+    b = Block(6)
+    x, res = b.batches[0]
+    want = b(x, res)
+    for t in (x, res, b.gate_w, b.bias, *b.shared):
+        t.requires_grad_()
+        with pytest.raises(ValueError, match="forward only"):
+            b(x, res)
+        t.requires_grad_(False)
+    for t in (x, res, b.gate_w, b.bias, *b.shared):
+        t.requires_grad_()
+    with torch.no_grad():
+        got = b(x, res)
+    for g, w in zip(got, want):
+        assert torch.equal(g, w) and not g.requires_grad

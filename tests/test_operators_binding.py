@@ -82,3 +82,19 @@ def test_the_binding_passes_the_reason_on(monkeypatch):
     x, w = torch.zeros(1, 16, dtype=torch.bfloat16).expand(4, 16), torch.zeros(8, 16, dtype=torch.bfloat16)
     with pytest.raises(pwb.PagedWeightError, match="rows of x are 0 elements apart"):
         pwb.linear(x, w)
+
+
+@needs_lib
+def test_tensors_that_require_a_gradient_are_refused(monkeypatch):
+    monkeypatch.setattr(pwb, "_here", lambda t, name: (0, None))
+    layer = pwb.PagedMoELayer(8, 128, 128, 2, max_tokens=4)
+    x, w = torch.zeros(2, 16).bfloat16().requires_grad_(), torch.zeros(8, 16).bfloat16()
+    logits = torch.zeros(2, 8, requires_grad=True)
+    tokens = torch.zeros(2, 128).bfloat16().requires_grad_()
+    calls = (lambda: pwb.linear(x, w), lambda: layer.route_gated(logits),
+             lambda: layer.moe_forward_routed(tokens, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)))
+    for call in calls:
+        with pytest.raises(ValueError, match="forward only"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # on to the next check
+            call()
