@@ -260,13 +260,14 @@ typedef struct {
 
 /* Dense product (router logits, shared experts): y = f(x w^T + bias) +
  * residual. bias fp32 or NULL, residual or NULL (it may be y itself, with
- * ldr = ldy); every pointer aligned to its element, y not overlapping x or
- * w. Operands are multiplied exactly and summed in fp32; everything after
- * in fp32, rounded once. Rows of x and w of any alignment and length
- * (16-byte aligned ones, with K a multiple of 8, are faster); ldx and ldw
- * below 2^22 where the tensor has more than one row. M = 0 or N = 0 does
- * nothing, K = 0 gives f(bias) + residual. Host checks only, no workspace,
- * no synchronisation; can be captured. Uses the current device. */
+ * ldr = ldy, and overlaps it in no other way); every pointer aligned to its
+ * element, y not overlapping x, w or bias. Operands are multiplied exactly
+ * and summed in fp32; everything after in fp32, rounded once. Rows of x and
+ * w of any alignment and length (16-byte aligned ones, with K a multiple of
+ * 8, are faster); ldx and ldw below 2^22 where the tensor has more than one
+ * row. M = 0 or N = 0 does nothing, K = 0 gives f(bias) + residual. Host
+ * checks only, no workspace, no synchronisation; can be captured. Uses the
+ * current device. */
 pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
                     const void* residual, void* y, void* stream);
 

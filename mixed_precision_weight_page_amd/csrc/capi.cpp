@@ -1161,6 +1161,8 @@ pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, co
     if (a.ldw < d.K) return row_bad("w", a.ldw, d.K);
     if (a.ldy < d.N) return row_bad("y", a.ldy, d.N);
     if (residual && a.ldr < d.N) return row_bad("residual", a.ldr, d.N);
+    if (residual && residual == y && a.ldr != a.ldy)
+        return bad("residual is y, but its rows are %lld elements apart and y's %lld", (long long)a.ldr, (long long)a.ldy);
     if ((d.M > 1 && a.ldx >= kMaxLd) || (rows > 1 && a.ldw >= kMaxLd))
         return bad("rows of x are %lld and of w %lld elements apart: must be below 2^22", (long long)a.ldx, (long long)a.ldw);
     if (!y || (d.K > 0 && (!x || !w))) return bad("null %s", !y ? "y" : !x ? "x" : "w");

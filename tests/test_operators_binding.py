@@ -98,3 +98,13 @@ def test_tensors_that_require_a_gradient_are_refused(monkeypatch):
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # on to the next check
             call()
+
+
+@needs_lib
+def test_a_residual_that_is_y_has_its_rows():
+    assert c_linear(r=FAKE, y=FAKE, ldr=8, ldy=9) == -1
+    assert b"residual is y" in pwb.lib().pw_last_error(None)
+    assert c_linear(r=FAKE, y=FAKE, ldr=9, ldy=8) == -1
+    # a single row has no distance to a next one (refused for its alignment only)
+    assert c_linear(r=ODD, y=ODD, M=1, ldr=8, ldy=9) == -1
+    assert b"aligned" in pwb.lib().pw_last_error(None)
