@@ -217,8 +217,12 @@ typedef struct {
  * and c = s + bias: the topk_group best groups stay (ties: lower group),
  * and of their experts the top_k with the largest c are chosen, in that
  * order (ties: lower expert; an expert whose c is NaN or -inf is not
- * chosen). The bias counts in the choice only. The choice is that of the
- * scores in fp64, also where fp32 could not tell two apart. Out: ids int32 [T, k] (-1 in slots left over), g fp32
+ * chosen). The bias counts in the choice only. Without a bias the order is
+ * the logits' (which is that of the exact scores), also for groups by their
+ * largest. With one, and for sums of two scores, c is compared as fp64 holds
+ * it, also where fp32 could not tell two apart: scores that fp64 rounds to
+ * one value (sigmoid logits above 37, softmax scores that underflow) tie.
+ * Out: ids int32 [T, k] (-1 in slots left over), g fp32
  * [T, k] (0 there; renormalised weights over an empty choice are 0) and
  * counts int32 [E] (pairs per expert; may be NULL). 0 <= T <= max_tokens;
  * n_group <= 64 divides E, topk_group E / n_group >= top_k, scale finite.

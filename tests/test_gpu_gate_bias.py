@@ -79,3 +79,24 @@ def test_groups_with_one_and_with_two_infinite_scores_are_equal(T, score):
             for topk_group in (1, 2):
                 for by in ("max", "top2"):
                     check(layer, logits, score=score, bias=bias, n_group=n_group, topk_group=topk_group, group_score=by)
+
+
+@pytest.mark.parametrize("T", [1, 30, 1100])
+def test_scores_that_fp64_rounds_to_one_value(T):
+    """Sigmoid scores of logits above 37 are 1 and softmax scores 800 below
+    the largest logit's 0 in fp64: without a bias the logits order them, with
+    one of zeros they tie."""
+    from mixed_precision_weight_page_amd import PagedMoELayer
+    layer = PagedMoELayer(8, 128, 128, 4, max_tokens=T)
+    for score, row in (("sigmoid", [40.0, 50.0, 38.0, 0.0, 45.0, 60.0, -1.0, 39.0]),
+                       ("softmax", [0.0, -900.0, -800.0, 1.0, -850.0, -825.0, 2.0, -875.0])):
+        logits = torch.tensor([row] * T)
+        for bias in (None, torch.zeros(8)):
+            ids, _, _ = layer.route_gated(logits.cuda(), score=score, bias=None if bias is None else bias.cuda())
+            want, _ = gate_oracle.token(row, LOW, 4, score=score, bias=None if bias is None else [0.0] * 8)
+            log(f"  {score} {'no bias' if bias is None else 'zeros'}: {want}")
+            assert ids.cpu().tolist() == [want] * T
+            live = sorted(range(8), key=lambda e: (-row[e], e)) if bias is None else None
+            assert live is None or want == live[:4]
+        tied = [e for e in range(8) if row[e] > 37] if score == "sigmoid" else [6, 3, 0, 1]
+        assert want == tied[:4]
