@@ -238,7 +238,7 @@ pw_status pw_route_gated(pw_ctx* ctx, const pw_gate_desc* gate, const void* logi
  * with an expert. An id outside [0, E) is a slot without one (its weight is
  * not used); an expert named twice by a token counts with both weights.
  * residual (NULL: none) and y [T, d] have type y_dtype, PW_F32 or PW_BF16;
- * residual may be y itself. Rounded once, to y's type; accuracy as
+ * residual may be y itself, and y (bf16) may be x: it is written last. Rounded once, to y's type; accuracy as
  * pw_moe_forward. 16-byte aligned x, y and residual. Works in the bound
  * workspace; records only kernel launches and clears its own counters, so a
  * captured call can be replayed (with a host tier as well). */

@@ -80,3 +80,141 @@ def test_tensors_that_require_a_gradient():
         got = b(x, res)
     for g, w in zip(got, want):
         assert torch.equal(g, w) and not g.requires_grad
+
+
+@pytest.mark.parametrize("T", [1, 48, 700])
+def test_a_captured_block_replays(T):
+    """Each replay, with new tokens, against the eager block bit for bit;
+    eager blocks of other sizes between the replays."""
+    b = Block(T)
+    x, res = (t.clone() for t in b.batches[0])
+    log(f"captured block T={T}")
+    b(x, res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = b(x, res)
+    for i, (nx, nr) in enumerate(b.batches[1:] + b.batches[:1]):
+        x.copy_(nx)
+        res.copy_(nr)
+        for o in out:
+            o.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        n = max(1, T // 3)
+        small = b(nx[:n], nr[:n])
+        assert bool(small[0].isfinite().all())
+        for g, w in zip(got, b(nx, nr)):
+            assert torch.equal(g, w), i
+
+
+@pytest.mark.parametrize("layout", ["eq2", "bitplane"])
+def test_two_graphs_of_one_layer(layout):
+    """Two captured blocks share the layer's workspace; replayed in turn, and
+    one twice in a row, each gives the eager block."""
+    b = Block(60, layout=layout)
+    xs = [b.batches[0][0].clone(), b.batches[1][0][:9].clone()]
+    rs = [b.batches[0][1].clone(), b.batches[1][1][:9].clone()]
+    for x, r in zip(xs, rs):
+        b(x, r)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, x, r in zip(graphs, xs, rs):
+        with torch.cuda.graph(g):
+            outs.append(b(x, r))
+    keep = []
+    for step, i in enumerate((0, 1, 1, 0, 0, 1)):
+        xs[i].copy_(b.batches[step % 3][0][:xs[i].shape[0]])
+        outs[i][0].fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs[i]]
+        keep.append((i, xs[i].clone(), got))
+        if step % 2:   # after every other replay the next one follows it directly
+            for j, x, o in keep:
+                for g, w in zip(o, b(x, rs[j])):
+                    assert torch.equal(g, w), step
+            keep = []
+
+
+def test_captured_given_routes_with_a_host_tier():
+    """Pages read through the device's cache of slots, decided at each replay
+    on the device."""
+    b = Block(40, k=2, d=256)
+    x, _ = b.batches[0]
+    gen = torch.Generator().manual_seed(3)
+    sets = [(torch.randn(40, 16, generator=gen).topk(2, dim=1)[1].int().cuda(), torch.rand(40, 2, generator=gen).cuda()) for _ in range(4)]
+    sets[2][0][:, :] = 5
+    sets[3][0][::2] = -1
+    want = [b.layer.moe_forward_routed(x, i, g) for i, g in sets]
+    b.layer.alloc_host_tier(16 * b.layer.slot_bytes())
+    b.layer.alloc_pool(5 * b.layer.slot_bytes())
+    b.layer.quantize_experts(b.bits)
+    ids, g = (t.clone() for t in sets[0])
+    assert torch.equal(b.layer.moe_forward_routed(x, ids, g), want[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = b.layer.moe_forward_routed(x, ids, g)
+    for n in (1, 2, 3, 0, 1):
+        ids.copy_(sets[n][0])
+        g.copy_(sets[n][1])
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[n]), n
+        assert torch.equal(b.layer.moe_forward_routed(x, *sets[3]), want[3])
+
+
+PATHS = [("own", 9, "eq2"), ("streaming", 40, "eq2"), ("bitplane", 40, "bitplane"), ("matrix_core", 700, "eq2")]
+
+
+@pytest.mark.parametrize("name,T,layout", PATHS, ids=[p[0] for p in PATHS])
+def test_what_tokens_without_experts_hold_does_not_matter(name, T, layout):
+    """Padded tokens (every id -1) may hold NaN and infinities: their rows
+    are the residual's, the others as with zeros there."""
+    b = Block(T, layout=layout)
+    x, res = b.batches[0]
+    gen = torch.Generator().manual_seed(T)
+    ids = torch.randn(T, 16, generator=gen).topk(4, dim=1)[1].int().cuda()
+    g = torch.rand(T, 4, generator=gen).cuda()
+    gone = torch.zeros(T, dtype=torch.bool, device="cuda")
+    gone[1::3] = True
+    ids[gone] = -1
+    g[gone] = float("nan")
+    clean, dirty = x.clone(), x.clone()
+    clean[gone] = 0.0
+    dirty[gone] = float("nan")
+    dirty[1] = float("inf")
+    a = b.layer.moe_forward_routed(clean, ids, g, res)
+    c = b.layer.moe_forward_routed(dirty, ids, g, res)
+    assert torch.equal(a, c) and torch.equal(c[gone], res[gone]) and bool(c.isfinite().all())
+
+
+@pytest.mark.parametrize("name,T,layout", PATHS, ids=[p[0] for p in PATHS])
+def test_the_tokens_own_rows_as_residual_and_output(name, T, layout):
+    """y and residual may be x: the sums are added last, after every expert
+    has read its tokens."""
+    b = Block(T, layout=layout)
+    x, _ = b.batches[0]
+    gen = torch.Generator().manual_seed(T)
+    ids = torch.randn(T, 16, generator=gen).topk(4, dim=1)[1].int().cuda()
+    g = torch.rand(T, 4, generator=gen).cuda()
+    want = b.layer.moe_forward_routed(x, ids, g, residual=x)
+    inside = x.clone()
+    assert b.layer.moe_forward_routed(inside, ids, g, residual=inside, y=inside) is inside
+    assert torch.equal(inside, want)
+
+
+@pytest.mark.parametrize("name,T,layout", PATHS, ids=[p[0] for p in PATHS])
+def test_every_slot_with_the_same_expert(name, T, layout):
+    """An expert named by all slots of every token counts with the sum of the
+    weights: as named once with that sum (quarters of whole numbers: exact)."""
+    b = Block(T, layout=layout)
+    x, _ = b.batches[0]
+    ids = torch.full((T, 4), 7, dtype=torch.int32, device="cuda")
+    g = (torch.randint(1, 9, (T, 4), generator=torch.Generator().manual_seed(T)).float() / 4).cuda()
+    once, total = torch.full_like(ids, -1), torch.zeros_like(g)
+    once[:, 0], total[:, 0] = 7, g.sum(dim=1)
+    assert torch.equal(b.layer.moe_forward_routed(x, ids, g), b.layer.moe_forward_routed(x, once, total))
