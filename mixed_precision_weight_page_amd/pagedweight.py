@@ -591,8 +591,10 @@ class PagedMoELayer:
         """A whole mixture-of-experts block on x bf16 [T, d]: router logits
         (linear with gate_w [E, d], in fp32), route_gated with the arguments
         in `gate`, the shared expert if given (w_gate_up [2 F, d] and w_down
-        [d, F], any F) and the routed experts, all added to residual. Returns
-        (y, ids, weights, pairs per expert)."""
+        [d, F], any F) and the routed experts, all added to residual, which
+        has out_dtype as y has. Rounded on the way: the shared expert's SwiGLU
+        rows to bf16, residual + shared expert to out_dtype (float32 keeps
+        that sum), y. Returns (y, ids, weights, pairs per expert)."""
         side = _other_stream(stream)
         if side is not None:
             tensors = (x, gate_w, gate_logit_bias, residual, y, gate.get("bias"), gate.get("mask"), *(shared or ()))

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import synth
-from layer_cases import log, make_layer
+from layer_cases import YTOL_MAX, cpu_threads, log, make_layer
+from test_gpu_linear import reference as linear_reference
+from test_gpu_routed import reference, weights64
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +15,7 @@ pytestmark = pytest.mark.gpu
 def _setup():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+    cpu_threads()
 
 
 GATE = dict(score="sigmoid", n_group=4, topk_group=2, group_score="top2", renorm=True, scale=2.5)
@@ -24,7 +27,8 @@ class Block:
     def __init__(self, T, seed=1, layout="eq2", **shape):
         wl = synth.WORKLOADS["decode_fine"].scaled(name="block", T=max(T, 1), **{**dict(E=16, d=256, F=384, k=4), **shape})
         self.wl = wl
-        self.layer, _ = make_layer(wl, synth.expert_weights(wl), max_tokens=max(T, 1), layout=layout)
+        self.masters = synth.expert_weights(wl)
+        self.layer, _ = make_layer(wl, self.masters, max_tokens=max(T, 1), layout=layout)
         self.bits = [(3, 4, 8)[e % 3] if layout == "eq2" else 1 + e % 8 for e in range(wl.E)]
         self.layer.quantize_experts(self.bits)
         gen = torch.Generator().manual_seed(seed)
@@ -218,3 +222,27 @@ def test_every_slot_with_the_same_expert(name, T, layout):
     once, total = torch.full_like(ids, -1), torch.zeros_like(g)
     once[:, 0], total[:, 0] = 7, g.sum(dim=1)
     assert torch.equal(b.layer.moe_forward_routed(x, ids, g), b.layer.moe_forward_routed(x, once, total))
+
+
+@pytest.mark.parametrize("T", [1, 48, 700])
+def test_a_block_in_fp32_keeps_the_shared_sum(T):
+    """With an fp32 residual and output only the shared expert's SwiGLU rows
+    are rounded on the way, to bf16 (half a step, 2^-8 of each; the products
+    around it within the dense product's bounds); the routed experts have the
+    layer's tolerance, per element of their largest. The residual is large,
+    so that a rounding of the sum to bf16 would go far past that."""
+    b = Block(T)
+    x, res = b.batches[0]
+    res = res.float() * 1000.0
+    y, ids, g, _ = b(x, res, out_dtype=torch.float32)
+    assert y.dtype == torch.float32
+    up, down = (w.cpu() for w in b.shared)
+    h, dh = linear_reference(x.cpu(), up, None, "swiglu", None)
+    dh = dh + 2.0 ** -8 * (h.abs() + dh)
+    S = (h.abs() + dh) @ down.double().abs().t()
+    routed = reference(x.cpu(), ids.cpu(), g.cpu(), None, weights64(b.masters, b.bits, "eq2"))
+    want = res.cpu().double() + h @ down.double().t() + routed
+    tol = dh @ down.double().abs().t() + (200 + 2) * 2.0 ** -23 * S + YTOL_MAX * routed.abs().max() + 2 * 2.0 ** -24 * (want.abs() + S)
+    err = (y.cpu().double() - want).abs()
+    log(f"block in fp32 T={T}: {float((err / tol).max()):.2f} of the bound, a rounding to bf16 {float((2.0 ** -8 * want.abs() / tol).max()):.0f}")
+    assert bool((err <= tol).all())
