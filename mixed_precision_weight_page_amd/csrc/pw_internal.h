@@ -105,8 +105,8 @@ struct Layout {
     uint64_t partial, stats_end;
     uint64_t dg, dg_bytes;   // the two counter sets of the streaming kernels' grouping (outside the
                              // bytes the statistics pass reuses; zeroed when the workspace is bound)
-    uint64_t rg;             // two more of the same size for forwards of given routes, which clear
-                             // what they count in at each call (so that a captured one can be replayed)
+    uint64_t rg;             // two more of the same size for forwards of given routes, whose combine
+                             // leaves them clear (a captured call clears them first, too)
     uint64_t total;
 };
 

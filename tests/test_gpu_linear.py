@@ -137,8 +137,8 @@ def test_large_tiles(M, N, K, act):
     run(M, N, K, act, bias=True, residual=True)
 
 
-# enough tiles of 256 x 256 for the phased kernel: every number of stages of
-# 32 K values up to its slots and past them, whole and ragged
+# enough tiles of 192 x 256 for the phased kernel: every number of stages of
+# 64 K values up to its slots and past them, whole and ragged
 @pytest.mark.parametrize("K", [0, 8, 32, 40, 64, 96, 128, 136, 168, 520])
 def test_phased_stages(K):
     run(4100, 2050, K, "none", bias=True)
