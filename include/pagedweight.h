@@ -269,9 +269,10 @@ typedef struct {
  * and summed in fp32; everything after in fp32, rounded once. Rows of x and
  * w of any alignment and length (16-byte aligned ones, with K a multiple of
  * 8, are faster); ldx and ldw below 2^22 where the tensor has more than one
- * row. M = 0 or N = 0 does nothing, K = 0 gives f(bias) + residual. Host
- * checks only, no workspace, no synchronisation; can be captured. Uses the
- * current device. */
+ * row. Products of more than 2^34 outputs, or of 2^28 columns and more, are
+ * refused where one launch cannot cover them. M = 0 or N = 0 does nothing,
+ * K = 0 gives f(bias) + residual. Host checks only, no workspace, no
+ * synchronisation; can be captured. Uses the current device. */
 pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
                     const void* residual, void* y, void* stream);
 

@@ -1184,6 +1184,8 @@ pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, co
     a.vec_out = (uintptr_t)y % (4 * ob) == 0 && (d.M == 1 || a.ldy % 4 == 0) &&
                 (!residual || ((uintptr_t)residual % (4 * ob) == 0 && (d.M == 1 || a.ldr % 4 == 0)));
     const hipError_t e = launch_linear(a, static_cast<hipStream_t>(stream));
+    if (e == hipErrorInvalidConfiguration)
+        return bad("M = %d, N = %d: the tiles of one launch would have 2^32 threads or more", d.M, d.N);
     return e == hipSuccess ? PW_OK : fail(nullptr, PW_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
 }
 

@@ -677,12 +677,21 @@ __global__ __launch_bounds__(512) void linear_phased_kernel(LinearArgs a) {
                           n0 + wn * (GLU ? RB / 2 : RB) * 16, m0 + wm * MB * 16);
 }
 
+// Workgroups of one launch, in whole eighths for the XCDs; 0 if they would
+// have 2^32 threads or more, which no launch takes.
+unsigned groups_of(int64_t tiles, int threads) {
+    const int64_t groups = (tiles + 7) / 8 * 8;
+    return groups < ((int64_t)1 << 32) / threads ? (unsigned)groups : 0u;
+}
+
 template <class T, int RB, int MB, bool GLU>
 hipError_t launch_phased(const LinearArgs& a, hipStream_t s) {
     constexpr int kOutN = GLU ? 16 * RB : 32 * RB, BM = 64 * MB;
     const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
+    const unsigned groups = groups_of(tiles, 512);
+    if (!groups) return hipErrorInvalidConfiguration;
     linear_phased_kernel<T, RB, MB, GLU>
-        <<<(unsigned)((tiles + 7) / 8 * 8), 512, (size_t)2 * (32 * RB + BM) * BK * 2 + 8 * 256, s>>>(a);
+        <<<groups, 512, (size_t)2 * (32 * RB + BM) * BK * 2 + 8 * 256, s>>>(a);
     return hipGetLastError();
 }
 
@@ -781,8 +790,10 @@ template <class T, int BM, int BN, int WM, int WN, int D, bool GLU>
 hipError_t launch_ring(const LinearArgs& a, hipStream_t s) {
     constexpr int kOutN = GLU ? BN / 2 : BN;
     const int64_t tiles = (int64_t)((a.N + kOutN - 1) / kOutN) * ((a.M + BM - 1) / BM);
+    const unsigned groups = groups_of(tiles, 64 * WM * WN);
+    if (!groups) return hipErrorInvalidConfiguration;
     linear_ring_kernel<T, BM, BN, WM, WN, D, GLU>
-        <<<(unsigned)((tiles + 7) / 8 * 8), 64 * WM * WN, (size_t)D * (BN + BM) * BK * 2, s>>>(a);
+        <<<groups, 64 * WM * WN, (size_t)D * (BN + BM) * BK * 2, s>>>(a);
     return hipGetLastError();
 }
 
@@ -875,6 +886,7 @@ template <class T, int RB, int MB, int D, bool GLU>
 hipError_t launch_stream(const LinearArgs& a, int waves, hipStream_t s) {
     constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
     const dim3 grid((unsigned)((a.N + kRowsOut - 1) / kRowsOut), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+    if (!groups_of(grid.x, 64 * waves)) return hipErrorInvalidConfiguration;
     const size_t lds = std::max((size_t)waves * D * (RB + MB) * 2048, (size_t)waves * RB * MB * 1024);
     linear_stream_kernel<T, RB, MB, D, GLU><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
@@ -884,6 +896,7 @@ template <class T, int RB, int MB, int D, bool GLU>
 hipError_t launch_skinny(const LinearArgs& a, int waves, hipStream_t s) {
     constexpr int kRowsOut = 16 * (GLU ? RB / 2 : RB);
     const dim3 grid((unsigned)((a.N + kRowsOut - 1) / kRowsOut), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+    if (!groups_of(grid.x, 64 * waves)) return hipErrorInvalidConfiguration;
     const size_t lds = (size_t)waves * RB * MB * 1024;
     linear_skinny_kernel<T, RB, MB, D, GLU><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
@@ -928,8 +941,9 @@ hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     const int64_t cols = GLU ? 2ll * a.N : a.N;
     auto tiles = [&](int64_t bn, int64_t bm) { return (cols + bn - 1) / bn * ((a.M + bm - 1) / bm); };
     if (!a.aligned) {
-        linear_any_kernel<T, GLU>
-            <<<(unsigned)((tiles(64, 64) + 7) / 8 * 8), 64 * kAnyWN * kAnyWM, 2 * 128 * BK * 2, s>>>(a);
+        const unsigned groups = groups_of(tiles(64, 64), 64 * kAnyWN * kAnyWM);
+        if (!groups) return hipErrorInvalidConfiguration;
+        linear_any_kernel<T, GLU><<<groups, 64 * kAnyWN * kAnyWM, 2 * 128 * BK * 2, s>>>(a);
         return hipGetLastError();
     }
     // The tile whose rounds (one workgroup per CU; two of the 64 x 64 tile)
