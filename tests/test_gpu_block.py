@@ -246,3 +246,27 @@ def test_a_block_in_fp32_keeps_the_shared_sum(T):
     err = (y.cpu().double() - want).abs()
     log(f"block in fp32 T={T}: {float((err / tol).max()):.2f} of the bound, a rounding to bf16 {float((2.0 ** -8 * want.abs() / tol).max()):.0f}")
     assert bool((err <= tol).all())
+
+
+def test_a_block_without_tokens():
+    b = Block(0)
+    x, res = b.batches[0]
+    y, ids, g, counts = b(x, res)
+    assert y.shape == (0, 256) and ids.shape == g.shape == (0, 4) and counts.cpu().tolist() == [0] * 16
+
+
+@pytest.mark.parametrize("name,T,layout", PATHS, ids=[p[0] for p in PATHS])
+def test_given_routes_while_forwards_are_timed(name, T, layout):
+    """pw_profile counts and times these forwards too, and changes none."""
+    b = Block(T, layout=layout)
+    x, res = b.batches[0]
+    ids = torch.randn(T, 16, generator=torch.Generator().manual_seed(T)).topk(4, dim=1)[1].int().cuda()
+    g = torch.full((T, 4), 0.25, device="cuda")
+    want = b.layer.moe_forward_routed(x, ids, g, res)
+    b.layer.profile(True)
+    for _ in range(3):
+        assert torch.equal(b.layer.moe_forward_routed(x, ids, g, res), want)
+    times = b.layer.profile_read()
+    b.layer.profile(False)
+    assert times["forwards"] == 3
+    assert all(times[n] > 0.0 for n in ("route_ms", "gate_up_ms", "down_ms", "combine_ms")), times
