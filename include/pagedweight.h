@@ -203,7 +203,7 @@ typedef struct {
     int32_t n_group;      /* G groups of E / G consecutive experts; 1: no groups  */
     int32_t topk_group;   /* groups that stay, 1 .. n_group                       */
     int32_t group_top2;   /* a group's score: 0 its largest choice score,
-                             1 the sum of its two largest                         */
+                             1 the sum of its two largest (of one, if alone)      */
     int32_t renorm;       /* 0: weight = score; 1: score over the chosen's sum    */
     float scale;          /* the weights are multiplied by it                     */
 } pw_gate_desc;
@@ -222,9 +222,9 @@ typedef struct {
  * largest. With one, and for sums of two scores, c is compared as fp64 holds
  * it, also where fp32 could not tell two apart: scores that fp64 rounds to
  * one value (sigmoid logits above 37, softmax scores that underflow) tie.
- * Out: ids int32 [T, k] (-1 in slots left over), g fp32
- * [T, k] (0 there; renormalised weights over an empty choice are 0) and
- * counts int32 [E] (pairs per expert; may be NULL). 0 <= T <= max_tokens;
+ * Out: ids int32 [T, k] (-1 in slots left over), g fp32 [T, k] (0 there;
+ * renormalised weights over an empty choice are 0) and counts int32 [E]
+ * (pairs per expert; may be NULL). 0 <= T <= max_tokens;
  * n_group <= 64 divides E, topk_group E / n_group >= top_k, scale finite.
  * T = 0 only clears counts. Needs neither pages nor a workspace, does not
  * synchronise, and can be captured and replayed. */
@@ -238,10 +238,11 @@ pw_status pw_route_gated(pw_ctx* ctx, const pw_gate_desc* gate, const void* logi
  * with an expert. An id outside [0, E) is a slot without one (its weight is
  * not used); an expert named twice by a token counts with both weights.
  * residual (NULL: none) and y [T, d] have type y_dtype, PW_F32 or PW_BF16;
- * residual may be y itself, and y (bf16) may be x: it is written last. Rounded once, to y's type; accuracy as
- * pw_moe_forward. 16-byte aligned x, y and residual. Works in the bound
- * workspace; records only kernel launches and clears its own counters, so a
- * captured call can be replayed (with a host tier as well). */
+ * residual may be y itself, and y (bf16) may be x: it is written last.
+ * Rounded once, to y's type; accuracy as pw_moe_forward. 16-byte aligned x, y
+ * and residual. Works in the bound workspace; records only kernel launches
+ * and clears its own counters, so a captured call can be replayed (with a
+ * host tier as well). */
 pw_status pw_moe_forward_routed(pw_ctx* ctx, const void* x, const int32_t* ids, const float* g, int32_t T,
                                 const void* residual, void* y, int32_t y_dtype, void* stream);
 
@@ -269,10 +270,10 @@ typedef struct {
  * and summed in fp32; everything after in fp32, rounded once. Rows of x and
  * w of any alignment and length (16-byte aligned ones, with K a multiple of
  * 8, are faster); ldx and ldw below 2^22 where the tensor has more than one
- * row. Products of more than 2^34 outputs, or of 2^28 columns and more, are
- * refused where one launch cannot cover them. M = 0 or N = 0 does nothing,
- * K = 0 gives f(bias) + residual. Host checks only, no workspace, no
- * synchronisation; can be captured. Uses the current device. */
+ * row. Products of more than 2^34 outputs, or with 2^28 or more rows or
+ * columns, are refused where one launch cannot cover them. M = 0 or N = 0
+ * does nothing, K = 0 gives f(bias) + residual. Host checks only, no
+ * workspace, no synchronisation; can be captured. Uses the current device. */
 pw_status pw_linear(const pw_linear_desc* desc, const void* x, const void* w, const float* bias,
                     const void* residual, void* y, void* stream);
 

@@ -167,7 +167,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _on_gpu(t, dev: int, name: str):
     if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient and this call is forward only: detach it, or call under torch.no_grad()")
+        raise ValueError(f"{name} requires a gradient, but this call is forward only: detach it, "
+                         "or call under torch.no_grad()")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.get_device() != dev:

@@ -115,6 +115,6 @@ def test_products_that_one_launch_cannot_cover_are_refused():
     for kw in (dict(M=1 << 24, N=1 << 24, ldr=1 << 24, ldy=1 << 24),                  # aligned tiles
                dict(M=1 << 20, N=1 << 20, K=15, ldx=15, ldw=15, ldy=1 << 20),        # rows of any alignment
                dict(M=1, N=1 << 30, K=15, ldx=15, ldw=15), dict(M=(1 << 31) - 1),    # one token; most tokens
-               dict(M=1, N=1 << 30, K=512, ldx=512, ldw=512)):
+               dict(M=1, N=1 << 30, K=512, ldx=512, ldw=512), dict(M=1 << 30, N=1, K=1, ldx=1, ldw=1, ldy=1)):
         assert c_linear(**kw) == -1, kw
         assert b"2^32" in pwb.lib().pw_last_error(None), kw
