@@ -221,11 +221,12 @@ typedef struct {
  * the logits' (which is that of the exact scores), also for groups by their
  * largest. With one, and for sums of two scores, c is compared as fp64 holds
  * it, also where fp32 could not tell two apart: scores that fp64 rounds to
- * one value (sigmoid logits above 37, softmax scores that underflow) tie.
- * Out: ids int32 [T, k] (-1 in slots left over), g fp32 [T, k] (0 there;
- * renormalised weights over an empty choice are 0) and counts int32 [E]
- * (pairs per expert; may be NULL). 0 <= T <= max_tokens;
- * n_group <= 64 divides E, topk_group E / n_group >= top_k, scale finite.
+ * one value (sigmoid logits above 37, scores that underflow: below 2^-1022
+ * some do) tie. Out: ids int32 [T, k] (-1 in slots left over), g fp32 [T, k]
+ * (0 there; renormalised weights are 0 over an empty choice, and softmax's
+ * beside an infinite logit that is not chosen) and counts int32 [E] (pairs
+ * per expert; may be NULL). 0 <= T <= max_tokens; n_group <= 64 divides E,
+ * topk_group E / n_group >= top_k, scale finite.
  * T = 0 only clears counts. Needs neither pages nor a workspace, does not
  * synchronise, and can be captured and replayed. */
 pw_status pw_route_gated(pw_ctx* ctx, const pw_gate_desc* gate, const void* logits, int32_t logits_dtype,

@@ -475,6 +475,9 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, bool valid,
         const float top = a.renorm ? lanes_fmax<L>(fmaxf(x0, x1)) : m;
         w0 = id0 < 0 ? 0.0f : (x0 == top ? 1.0f : exp_neg(x0 - top));
         w1 = id1 < 0 ? 0.0f : (x1 == top ? 1.0f : exp_neg(x1 - top));
+        // beside an infinite logit that is not chosen every score is 0, and so
+        // is their sum (m is not taken where the largest logit is always chosen)
+        if (a.renorm && m == INFINITY && top < INFINITY) w0 = w1 = 0.0f;
     } else {
         // s = e^min(x, 0) / (1 + e^-|x|); renormalised weights leave out the
         // common power of e, so that they are right where every s underflows

@@ -100,3 +100,22 @@ def test_scores_that_fp64_rounds_to_one_value(T):
             assert live is None or want == live[:4]
         tied = [e for e in range(8) if row[e] > 37] if score == "sigmoid" else [6, 3, 0, 1]
         assert want == tied[:4]
+
+
+@pytest.mark.parametrize("T", [1, 16, 30, 70, 1100])
+def test_softmax_beside_an_infinite_logit_that_is_not_chosen(T):
+    """Its score is 1 and every other 0: the weights of the others are 0,
+    renormalised as well (a sum of 0 gives weights of 0). Where it is chosen
+    it has all the weight."""
+    from mixed_precision_weight_page_amd import PagedMoELayer
+    for E, k in ((8, 3), (96, 8)):
+        layer = PagedMoELayer(E, 128, 128, k, max_tokens=T)
+        logits = tied(T, E, T + E)
+        logits[:, 5] = math.inf
+        for b5 in (0.0, -4.0, -math.inf, math.nan):
+            bias = torch.zeros(E)
+            bias[5] = b5
+            for renorm in (False, True):
+                check(layer, logits, bias=bias, renorm=renorm, scale=2.5)
+                check(layer, logits, bias=bias, renorm=renorm, n_group=2, topk_group=2)
+                check(layer, logits, renorm=renorm)
