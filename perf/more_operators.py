@@ -95,20 +95,19 @@ def _draw_quantize(rng):
                      rng.random() < 0.5, rng.choice([0, 0, 3]))
 
 
-# 8-bit products come out in 16 bits, as the next operator reads them
 ACTS = ["none", "none", "relu", "gelu", "gelu_tanh", "silu", "sigmoid", "swiglu", "swiglu"]
 
 
 def _draw_linear8(rng):
     return _linear8(_log(rng, 1, 8192), _width(rng, 16, 8192), _width(rng, 64, 8192), rng.choice(ACTS),
-                    rng.choice(["bf16", "bf16", "f16"]), rng.random() < 0.5, rng.random() < 0.5, rng.choice([0, 0, 0, 16, 3]))
+                    rng.choice(["bf16", "bf16", "f16", "f32"]), rng.random() < 0.5, rng.random() < 0.5, rng.choice([0, 0, 0, 16, 3]))
 
 
 def _draw_grouped(rng):
     R = _log(rng, 1, 24576)
     dtype = rng.choice(["bf16", "f16", "e4m3", "e4m3"])
     return _grouped(R, _log(rng, 1, 128), _width(rng, 32, 4096), _width(rng, 64, 4096), dtype, rng.choice(ACTS),
-                    rng.choice(["bf16", "f16" if dtype == "e4m3" else "f32"]), rng.random() < 0.3, rng.random() < 0.3, rng.choice([0.0, 0.5, 1.0]),
+                    rng.choice(["bf16", "f32"]), rng.random() < 0.3, rng.random() < 0.3, rng.choice([0.0, 0.5, 1.0]),
                     rng.choice([0, 0, 1, 37]), rng.choice([0, 0, (R + 3) // 4]))
 
 
