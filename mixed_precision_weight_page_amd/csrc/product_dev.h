@@ -9,7 +9,10 @@
 // 64 ones alike) cuts each product off at 2^-13 of the power of two under the
 // largest of the eight whose K values share 8 bytes. That is 1.5e-5 of the
 // norm of the sum for normally distributed operands, where e4m3 has rounded
-// each by up to 2^-4; 16-bit instructions, exact, have half the rate.
+// each by up to 2^-4 (rows with a few channels twenty times the others: 3.5e-5).
+// A 16-bit y rounds by far more; for an fp32 y the same kernels run with
+// E4M3Full operands, whose products are exact, on 16-bit instructions of half
+// the rate.
 // With SwiGLU the gate and the up rows have row blocks of their own, each from
 // its first row.
 //
@@ -28,8 +31,13 @@ namespace {
 struct E4M3 {   // one OCP e4m3 value
     uint8_t bits;
 };
+struct E4M3Full {   // the same, for products of which nothing may be lost
+    uint8_t bits;
+};
 template <class T>
-constexpr bool kEight = std::is_same<T, E4M3>::value;
+constexpr bool kFull = std::is_same<T, E4M3Full>::value;
+template <class T>
+constexpr bool kEight = std::is_same<T, E4M3>::value || kFull<T>;
 template <class T>
 constexpr int kStage = 128 / (int)sizeof(T);   // K values per step: 128-byte rows in LDS
 
@@ -44,6 +52,25 @@ __device__ __forceinline__ f32x4 mma8(const u32x4& a0, const u32x4& a1, const u3
         __builtin_bit_cast(i32x8, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7)), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+// 32 codes as fp16, which holds every e4m3 value (and their products are exact
+// in fp32): 8 to each of four 16 x 16 x 32 products, which together cover a
+// lane's K-slots as mma8 does.
+struct Halves {
+    u32x4 v[4];
+};
+__device__ __forceinline__ Halves halves_of(const u32x4& a0, const u32x4& a1) {
+    Halves h;
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t word = i < 4 ? a0[i & 3] : a1[i & 3];
+        h.v[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false));
+        h.v[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true));
+    }
+#endif
+    return h;
+}
+
 // 16 bytes from p, of any alignment; left: bytes of the row from p on, zeros
 // past them
 typedef unsigned int u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
@@ -55,6 +82,40 @@ __device__ __forceinline__ u32x4 load_bytes(const uint8_t* p, int left) {
     for (int i = 0; i < 16; ++i)
         if (i < left) u[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
     return u;
+}
+
+// acc += (fw fx^T) f, block by block; f[h][j]: the scales' product for token
+// block j and the gate (or only) and up rows.
+template <class T, int RB, int MB, bool GLU>
+__device__ __forceinline__ void scaled_blocks(f32x4 (&acc)[RB][MB], const u32x4 (&fw)[RB][2], const u32x4 (&fx)[MB][2],
+                                              const float (&f)[2][MB]) {
+    auto join = [&](int i, int j, const f32x4& p) {
+        const float s = f[GLU ? i & 1 : 0][j];
+        acc[i][j] = __builtin_elementwise_fma(p, f32x4{s, s, s, s}, acc[i][j]);
+    };
+    if constexpr (kFull<T>) {
+        Halves x[MB];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) x[j] = halves_of(fx[j][0], fx[j][1]);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const Halves w = halves_of(fw[i][0], fw[i][1]);
+            f32x4 p[MB];
+#pragma unroll
+            for (int j = 0; j < MB; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < MB; ++j) p[j] = mma<_Float16>(w.v[q], x[j].v[q], p[j]);
+#pragma unroll
+            for (int j = 0; j < MB; ++j) join(i, j, p[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < MB; ++j) join(i, j, mma8(fw[i][0], fw[i][1], fx[j][0], fx[j][1]));
+    }
 }
 
 // ---- groups ----
@@ -284,16 +345,14 @@ __global__ __launch_bounds__(64 * kAnyWN * kAnyWM) void product_any_kernel(Produ
         }
         if constexpr (kEight<T>) {
             const float sg = wg[s * a.ws_block], su = GLU ? wu[s * a.ws_block] : 0.0f;
+            float f[2][MB];
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
                 const float sx = xs[j] ? xs[j][s * a.xs_block] : 0.0f;
-#pragma unroll
-                for (int i = 0; i < RB; ++i) {
-                    const float f = sx * (GLU && (i & 1) ? su : sg);
-                    const f32x4 p = mma8(fw[i][0], fw[i][1], fx[j][0], fx[j][1]);
-                    acc[i][j] = __builtin_elementwise_fma(p, f32x4{f, f, f, f}, acc[i][j]);
-                }
+                f[0][j] = sx * sg;
+                f[1][j] = sx * su;
             }
+            scaled_blocks<T, RB, MB, GLU>(acc, fw, fx, f);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -407,22 +466,6 @@ struct ScaleCopies {
     }
 };
 
-// acc += (fw fx^T) f, block by block, for weight blocks lo .. hi - 1.
-// f[h][j]: the scales' product for token block j and the gate (or only) and
-// up rows.
-template <int LO, int HI, int RB, int MB, bool GLU>
-__device__ __forceinline__ void scaled_blocks(f32x4 (&acc)[RB][MB], const u32x4 (*fw)[2], const u32x4 (&fx)[MB][2],
-                                              const float (&f)[2][MB]) {
-#pragma unroll
-    for (int i = LO; i < HI; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j) {
-            const f32x4 p = mma8(fw[i - LO][0], fw[i - LO][1], fx[j][0], fx[j][1]);
-            const float s = f[GLU ? i & 1 : 0][j];
-            acc[i][j] = __builtin_elementwise_fma(p, f32x4{s, s, s, s}, acc[i][j]);
-        }
-}
-
 // BN weight rows x BM rows of x, WN x WM waves, K in steps of 128 bytes
 // through a ring of D LDS slots, one barrier a step, so that D - 2 steps'
 // copies are on their way while one is multiplied. Bound by those copies, and
@@ -498,7 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_ring_kernel(ProductArgs 
                     f[0][j] = sx * sg;
                     f[1][j] = sx * su;
                 }
-                scaled_blocks<0, RB, RB, MB, GLU>(acc, fw, fx, f);
+                scaled_blocks<T, RB, MB, GLU>(acc, fw, fx, f);
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -748,7 +791,7 @@ __global__ __launch_bounds__(512) void product_phased_kernel(ProductArgs a) {
 // experts, 2048 -> 2 x 768 bf16 117 us, 5.3 TB/s.
 // Grouped: blockIdx.y is the expert, its rows are taken 16 MB at a time.
 template <class T, int RB, int MB, int D, bool GLU, bool GRP>
-__global__ __launch_bounds__(1024) void product_stream_kernel(ProductArgs a) {
+__global__ __launch_bounds__(kFull<T> && MB == 4 ? 256 : 1024) void product_stream_kernel(ProductArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint16_t ring_lds[];   // [waves][D][slot]
     constexpr int kBlock = 16 * 64, kB = (int)sizeof(T);
     constexpr int kSC = kEight<T> ? 2 : 0;   // copies of scales, 64 floats each: of the rows of x, of the weights (gate, up)
@@ -857,7 +900,7 @@ __global__ __launch_bounds__(1024) void product_stream_kernel(ProductArgs a) {
             copy(i + D, slot);
             slot = slot + 1 == D ? 0 : slot + 1;
             if constexpr (kEight<T>) {
-                scaled_blocks<0, RB, RB, MB, GLU>(acc, fw, fx, f);
+                scaled_blocks<T, RB, MB, GLU>(acc, fw, fx, f);
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -941,17 +984,21 @@ hipError_t launch_stream(const ProductArgs& a, int waves, hipStream_t s) {
 // experts, 4096 -> 2048 bf16: 262, 197, 218, and 186 with 128 rows x 256; in
 // e4m3 158, 96 (two workgroups on a CU), 113; 24576 rows of 64 experts, 4096
 // -> 2816 e4m3: 770, 470, 435; of one: 4096 -> 4096 bf16 775 (128 x 256) and
-// 668 (256 x 256).
+// 668 (256 x 256). E4M3Full has no 256 x 256 tile (its operands as fp16 leave
+// no registers for one): 8192 x 4096 x 4096 385, 318, 263 (two workgroups on a
+// CU), 254; 1024 x 4096 x 4096 57, 44, 43, 62.
 struct TileCost {
     int bm, bn, at_once;           // rows of x, weight rows; workgroups on a CU
     double fixed, alone, shared;   // time of a tile: fixed + S times alone, or shared where a CU has two
 };
 template <class T>
+constexpr int kTileKinds = kFull<T> ? 4 : 5;
+template <class T>
 constexpr TileCost kTiles[5] = {
-    {64, 64, 2, 3.0, kEight<T> ? 0.44 : 0.33, kEight<T> ? 0.53 : 0.50},
-    {128, 128, 1, 4.0, kEight<T> ? 0.66 : 0.65, 0.0},
-    {128, 128, 2, 4.0, kEight<T> ? 0.68 : 0.90, kEight<T> ? 1.25 : 1.35},
-    {128, 256, 1, 5.0, kEight<T> ? 1.15 : 0.95, 0.0},
+    {64, 64, 2, 3.0, kFull<T> ? 0.52 : kEight<T> ? 0.44 : 0.33, kFull<T> ? 0.66 : kEight<T> ? 0.53 : 0.50},
+    {128, 128, 1, 4.0, kFull<T> ? 1.10 : kEight<T> ? 0.66 : 0.65, 0.0},
+    {128, 128, 2, 4.0, kFull<T> ? 1.12 : kEight<T> ? 0.68 : 0.90, kFull<T> ? 1.93 : kEight<T> ? 1.25 : 1.35},
+    {128, 256, 1, 5.0, kFull<T> ? 1.80 : kEight<T> ? 1.15 : 0.95, 0.0},
     {256, 256, 1, kEight<T> ? 8.0 : 10.0, 1.6, 0.0},
 };
 
@@ -965,7 +1012,7 @@ TileChoice choose_tile(const ProductArgs& a) {
     const double S = (a.K + kStage<T> - 1) / kStage<T>;
     const double groups = GRP ? std::min(a.E, a.M) : 1, mean = a.M / groups;
     TileChoice best{0, 0.0};
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < kTileKinds<T>; ++i) {
         const TileCost& t = kTiles<T>[i];
         // an expert's rows are not known here: on average half a tile more than they fill
         const double rows = GRP && groups > 1 ? groups * std::max(1.0, mean / t.bm + 0.5) : (double)(((int64_t)a.M + t.bm - 1) / t.bm);
@@ -986,8 +1033,10 @@ hipError_t launch_tiles(const ProductArgs& a, int tile, hipStream_t s) {
         case 1: return launch_ring<T, 128, 128, 2, 4, 4, GLU, GRP>(a, s);
         case 2: return launch_ring<T, 128, 128, 2, 4, 2, GLU, GRP>(a, s);
         case 3: return launch_ring<T, 128, 256, 2, 4, 3, GLU, GRP>(a, s);
-        default: return launch_phased<T, GLU, GRP>(a, s);
+        default: break;
     }
+    if constexpr (kTileKinds<T> == 5) return launch_phased<T, GLU, GRP>(a, s);
+    return hipErrorInvalidValue;   // choose_tile names no such tile
 }
 
 // Few rows an expert (on average): the weights are streamed. 512 rows of 64

@@ -254,7 +254,7 @@ struct LinearArgs {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
 // Products of e4m3 operands with block scales, and products grouped by
-// expert (product_dev.h; kernels_fp8.hip, kernels_grouped*.hip). Grouped: M
+// expert (product_dev.h, fp8_dev.h; kernels_fp8*.hip, kernels_grouped*.hip). Grouped: M
 // rows in all, rows offsets[e] .. offsets[e + 1] of x (or, with `rows`, the
 // rows of x that these name) by expert e's weights. LinearArgs' in_dtype is a
 // pw_dtype or PW_E4M3.
@@ -266,9 +266,11 @@ struct ProductArgs : LinearArgs {
     int E, x_rows;                  // rows: x's
     int64_t w_expert;               // elements between two experts' weights
 };
-hipError_t launch_linear_fp8(const ProductArgs& a, hipStream_t s);
+hipError_t launch_linear_fp8(const ProductArgs& a, hipStream_t s);   // of e4m3 operands; full: fp32 y
+hipError_t launch_linear_fp8_full(const ProductArgs& a, hipStream_t s);
 hipError_t launch_grouped(const ProductArgs& a, hipStream_t s);
 hipError_t launch_grouped_fp8(const ProductArgs& a, hipStream_t s);
+hipError_t launch_grouped_fp8_full(const ProductArgs& a, hipStream_t s);
 
 // Pairs in expert order, and their products joined to tokens (kernels_pairs.hip)
 struct JoinArgs {

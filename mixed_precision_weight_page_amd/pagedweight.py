@@ -529,7 +529,9 @@ def linear_fp8(x: Fp8, w: Fp8, bias: Optional[torch.Tensor] = None, act: str = "
     [M, ceil(K / 128)] (quantize_fp8, rms_norm), w: codes [N, K] and scales
     [ceil(N / 128), ceil(K / 128)] (quantize_fp8 with block "tile"); with act
     "swiglu" codes [2 N, K] and the gate's scale rows, then the up half's.
-    out_dtype: default y's or residual's type, else bfloat16. Else as linear."""
+    out_dtype: default y's or residual's type, else bfloat16. A float32 y is
+    summed from exact products, a 16-bit one from products to 2^-13 of the
+    largest of their eight neighbours along K, in half the time. Else as linear."""
     if stream is None and _fast is not None:
         got = _fast.linear_fp8(x, w, bias, ACTIVATIONS.get(act), residual, y, out_dtype)
         if got is not None:
