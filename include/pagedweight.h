@@ -312,8 +312,9 @@ typedef struct {
  * both NULL (h = x is then not written); h may be residual itself, and y may
  * be x, with the same row distance. PW_E4M3: y holds codes of h w r, scale
  * [T, ceil(n / 128)] their scales (the codes are those of h w in fp32: r
- * scales a whole row). Rows whose squares leave fp32's range are summed in
- * fp64. */
+ * scales a whole row). Rows whose squares or whose r leave fp32's range, and
+ * blocks of codes whose h w does, go through fp64 (their codes are those of h w
+ * itself), so y is finite wherever its type holds it. */
 pw_status pw_rms_norm(const pw_rms_norm_desc* desc, const void* x, const void* weight, const void* residual,
                       void* h, void* y, float* scale, void* stream);
 

@@ -4,9 +4,11 @@
 //
 // Norm of a row: h = x + residual, rounded to the residual's type, which is
 // written; r = 1 / sqrt(mean(h^2) + eps); y = h w r, in fp32 from the written
-// h on and rounded once. In 8 bits: z = h w in fp32 (exact for 16-bit h and
-// w), m = max |z| over 128 columns, codes 448 z / m and the scale r m / 448: r
-// cancels from the codes, so they do not hang on its rounding.
+// h on (as (h r) w: h r is at most sqrt(n), so no product leaves fp32's range
+// before y does) and rounded once. In 8 bits: z = h w in fp32 (exact for 16-bit h
+// and w), m = max |z| over 128 columns, codes 448 z / m and the scale r m / 448: r
+// cancels from the codes, so they do not hang on its rounding. Rows whose sum of
+// squares leaves fp32's range, and blocks whose z do, go through fp64.
 //
 // Bound by the bytes: each element is read once, held in registers over the
 // reduction, and written once. 16384 x 4096 bf16 with a bf16 residual and e4m3
@@ -73,11 +75,15 @@ __device__ __forceinline__ void put8(T* p, int left, const float (&f)[8]) {
 }
 
 // Eight columns of 16 neighbouring lanes are a block: its largest magnitude,
-// the codes, and (the first lane) the scale.
+// the codes (of t = 448 z / m), and (the first lane) the scale.
+__device__ __forceinline__ void quotients(float (&t)[8], const float (&z)[8], const E4m3Factor& f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = e4m3_scaled(z[e], f);
+}
 template <bool VEC>
-__device__ __forceinline__ void put_codes(uint8_t* p, int left, const float (&z)[8], const E4m3Factor& f) {
-    const uint32_t a = e4m3_pack(e4m3_scaled(z[0], f), e4m3_scaled(z[1], f), e4m3_scaled(z[2], f), e4m3_scaled(z[3], f));
-    const uint32_t b = e4m3_pack(e4m3_scaled(z[4], f), e4m3_scaled(z[5], f), e4m3_scaled(z[6], f), e4m3_scaled(z[7], f));
+__device__ __forceinline__ void put_codes(uint8_t* p, int left, const float (&t)[8]) {
+    const uint32_t a = e4m3_pack(t[0], t[1], t[2], t[3]);
+    const uint32_t b = e4m3_pack(t[4], t[5], t[6], t[7]);
     if (VEC) {
         *reinterpret_cast<u32x2*>(p) = u32x2{a, b};
         return;
@@ -103,6 +109,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
     return v;
+}
+
+// The quotients 448 h w / m and the scale r m / 448 of a block whose h w, or
+// whose row's r, fp32 does not hold (h comes times 2^-shift). NaN counts no more
+// here than there.
+__device__ __forceinline__ void wide_block(const float (&h)[8], const float (&w)[8], float r, int shift, float (&q)[8], float& scale) {
+    double m = ldexp((double)kE4m3Least, -shift);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmax(m, fabs((double)h[e] * (double)w[e]));
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = fmax(m, __shfl_xor(m, d));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = (float)((double)kE4m3Top * ((double)h[e] * (double)w[e]) / m);
+    scale = (float)(m * (double)r / (double)kE4m3Top);
 }
 
 // blockDim.x / 64 waves a row, V pieces of 8 elements a lane: piece i of lane
@@ -165,7 +185,9 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
     auto add = [](float p, float q) { return p + q; };
     sum = over_row(sum, add, wave_sum);
     float r;
-    if (sum < 0x1p+120f && sum > 0x1p-90f) {
+    int shift = 0;   // h is held times 2^-shift
+    const bool wide = !(sum < 0x1p+120f && sum > 0x1p-90f);
+    if (!wide) {
         r = 1.0f / sqrtf(sum / (float)a.n + a.eps);
     } else {
         // squares that overflow, or vanish beside a small eps: again in fp64,
@@ -185,33 +207,50 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
             s = 0.0;
             for (int w = 0; w < waves; ++w) s += wide[w];
         }
-        r = (float)(1.0 / sqrt(s / a.n + (double)a.eps));
+        // r itself may leave fp32's range: its power of two goes to h
+        const double r64 = 1.0 / sqrt(s / a.n + (double)a.eps);
+        const bool usual = r64 > 0.0 && r64 < (double)INFINITY;
+        shift = usual ? -__builtin_amdgcn_readfirstlane(ilogb(r64)) : 0;
+        r = (float)ldexp(r64, shift);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = ldexpf(h[i][e], -shift);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (64 * (i * waves + wave) + lane);
-        if (a.weight && c < a.n) {
-            auto times = [&](auto w, auto type) {
-                typedef decltype(type) W;
-                if (VEC) w.load(reinterpret_cast<const W*>(a.weight) + c);
-                else w.load_some(reinterpret_cast<const W*>(a.weight) + c, a.n - c);
+        float w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] *= w[e];
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        if (a.weight && c < a.n) {
+            auto take = [&](auto v, auto type) {
+                typedef decltype(type) W;
+                if (VEC) v.load(reinterpret_cast<const W*>(a.weight) + c);
+                else v.load_some(reinterpret_cast<const W*>(a.weight) + c, a.n - c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = v[e];
             };
-            if (a.w_dtype == PW_F32) times(Eight<float>{}, 0.0f);
-            else if (a.w_dtype == PW_BF16) times(Eight<__bf16>{}, (__bf16)0.0f);
-            else times(Eight<_Float16>{}, (_Float16)0.0f);
+            if (a.w_dtype == PW_F32) take(Eight<float>{}, 0.0f);
+            else if (a.w_dtype == PW_BF16) take(Eight<__bf16>{}, (__bf16)0.0f);
+            else take(Eight<_Float16>{}, (_Float16)0.0f);
         }
         if (a.y_dtype == PW_E4M3) {
-            const float m = fmaxf(row_max(largest(h[i])), kE4m3Least);
+            float z[8], q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = h[i][e] * w[e];
+            const float m = fmaxf(row_max(largest(z)), kE4m3Least);
+            float scale = m * r / kE4m3Top;
+            if (!wide && m < INFINITY) quotients(q, z, e4m3_factor(m));
+            else wide_block(h[i], w, r, shift, q, scale);   // (the same for a block's 16 lanes)
             if (c >= a.n) continue;
-            put_codes<VEC>(reinterpret_cast<uint8_t*>(a.y) + t * a.ldy + c, a.n - c, h[i], e4m3_factor(m));
-            if (!(lane & 15)) a.scale[t * a.s_row + (c / kScaleBlock) * a.s_block] = m * r / kE4m3Top;
+            put_codes<VEC>(reinterpret_cast<uint8_t*>(a.y) + t * a.ldy + c, a.n - c, q);
+            if (!(lane & 15)) a.scale[t * a.s_row + (c / kScaleBlock) * a.s_block] = scale;
             continue;
         }
         if (c >= a.n) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] *= r;
+        for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * r * w[e];
         const int64_t at = t * a.ldy + c;
         if (a.y_dtype == PW_F32) put8<VEC>(reinterpret_cast<float*>(a.y) + at, a.n - c, h[i]);
         else if (a.y_dtype == PW_BF16) put8<VEC>(reinterpret_cast<__bf16*>(a.y) + at, a.n - c, h[i]);
@@ -271,7 +310,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
             else v[i].load_some(x + (int64_t)row * a.ldx + c, a.K - c);
         }
     }
-    float f[8];
+    float f[8], t[8];
     auto values = [&](int i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = v[i][j];
@@ -299,7 +338,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
             factor = e4m3_factor(m);
         }
         if (row >= a.M || c >= a.K) continue;
-        put_codes<VEC>(out + (int64_t)row * a.ldq + c, a.K - c, f, factor);
+        quotients(t, f, factor);
+        put_codes<VEC>(out + (int64_t)row * a.ldq + c, a.K - c, t);
         if (!TILE && !(tid & 15)) scale[row * a.s_row + kb * a.s_block] = m / kE4m3Top;
     }
 }
