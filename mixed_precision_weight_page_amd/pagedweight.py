@@ -298,16 +298,27 @@ def _other_stream(stream):
     return torch.cuda.default_stream() if raw == 0 else torch.cuda.ExternalStream(raw)
 
 
-def _call_on(stream, tensors, call):
+def _record(arg, stream):
+    """Tensors of an argument, or of pairs and sequences of them, are not
+    reused before `stream` is done with them."""
+    if isinstance(arg, torch.Tensor):
+        if arg.is_cuda:
+            arg.record_stream(stream)
+    elif isinstance(arg, (tuple, list)):
+        for a in arg:
+            _record(a, stream)
+
+
+def _call_on(stream, args, call):
     """call() with `stream` as the current one: what it allocates belongs to
-    that stream, and what it reads or writes is not reused before the stream
-    is done with it."""
-    with torch.cuda.stream(stream):
-        out = call()
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-    return out
+    that stream, and what it reads or writes (among args, which only call
+    itself checks) is not reused before the stream is done with it, also where
+    a later part of the call raises."""
+    try:
+        with torch.cuda.stream(stream):
+            return call()
+    finally:
+        _record(args, stream)
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
@@ -420,7 +431,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
             return Fp8(*got) if residual is None else (Fp8(got[0], got[1]), got[2])
     side = _other_stream(stream)
     if side is not None:
-        return _call_on(side, (x, weight, residual, h, *(out if _is_pair(out) else (out,))),
+        return _call_on(side, (x, weight, residual, h, out),
                         lambda: rms_norm(x, weight, eps, residual, h, out, out_dtype))
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-d tensor")
@@ -485,7 +496,7 @@ def quantize_fp8(x: torch.Tensor, block: str = "row", out=None, stream=None) -> 
             return Fp8(*got)
     side = _other_stream(stream)
     if side is not None:
-        return _call_on(side, (x, *(out or ())), lambda: quantize_fp8(x, block, out))
+        return _call_on(side, (x, out), lambda: quantize_fp8(x, block, out))
     if block not in ("row", "tile"):
         raise ValueError("block must be 'row' or 'tile'")
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
@@ -538,7 +549,7 @@ def linear_fp8(x: Fp8, w: Fp8, bias: Optional[torch.Tensor] = None, act: str = "
             return got if y is None else y
     side = _other_stream(stream)
     if side is not None:
-        return _call_on(side, (*x, *w, bias, residual, y), lambda: linear_fp8(x, w, bias, act, residual, y, out_dtype))
+        return _call_on(side, (x, w, bias, residual, y), lambda: linear_fp8(x, w, bias, act, residual, y, out_dtype))
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
     if not _is_pair(x) or not _is_pair(w):
@@ -589,8 +600,8 @@ def grouped_linear(x: Union[torch.Tensor, Fp8], offsets: torch.Tensor, w: Union[
     eight = _is_pair(x)
     side = _other_stream(stream)
     if side is not None:
-        tensors = (*(x if eight else (x,)), offsets, *(w if _is_pair(w) else (w,)), bias, residual, y, rows)
-        return _call_on(side, tensors, lambda: grouped_linear(x, offsets, w, bias, act, residual, y, rows, out_dtype))
+        return _call_on(side, (x, offsets, w, bias, residual, y, rows),
+                        lambda: grouped_linear(x, offsets, w, bias, act, residual, y, rows, out_dtype))
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
     if eight != _is_pair(w):
@@ -691,13 +702,14 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, g: torch.Tensor, w_gate_up: 
     out_dtype: default y's, residual's or x's type."""
     side = _other_stream(stream)
     if side is not None:
-        tensors = (x, ids, g, *(w_gate_up if _is_pair(w_gate_up) else (w_gate_up,)), *(w_down if _is_pair(w_down) else (w_down,)),
-                   residual, y)
-        return _call_on(side, tensors, lambda: moe_experts(x, ids, g, w_gate_up, w_down, residual, y, out_dtype))
+        return _call_on(side, (x, ids, g, w_gate_up, w_down, residual, y),
+                        lambda: moe_experts(x, ids, g, w_gate_up, w_down, residual, y, out_dtype))
     eight = _is_pair(w_gate_up)
     if eight != _is_pair(w_down):
         raise ValueError("w_gate_up and w_down must both be tensors or both Fp8")
     up, down = (w_gate_up[0], w_down[0]) if eight else (w_gate_up, w_down)
+    if not all(isinstance(t, torch.Tensor) for t in (x, ids, up, down)):
+        raise ValueError("x, ids, w_gate_up and w_down must be tensors (8-bit weights: codes and scales)")
     if up.dim() != 3 or down.dim() != 3 or x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError("x must be [T, d], ids [T, k], w_gate_up [E, 2 F, d] and w_down [E, d, F]")
     E, d = up.shape[0], x.shape[1]
@@ -1036,10 +1048,8 @@ class PagedMoELayer:
         pairs per expert)."""
         side = _other_stream(stream)
         if side is not None:
-            flat = [t for p in (*(shared or ()), *(experts or ())) for t in (p if _is_pair(p) else (p,))]
-            tensors = (x, gate_w, gate_logit_bias, residual, y, gate.get("bias"), gate.get("mask"), *flat,
-                       *((norm[0],) if norm is not None else ()))
-            return _call_on(side, tensors, lambda: self.moe_block(x, gate_w, gate_logit_bias, shared, residual, y,
+            args = (x, gate_w, gate_logit_bias, shared, residual, y, norm, experts, tuple(gate.values()))
+            return _call_on(side, args, lambda: self.moe_block(x, gate_w, gate_logit_bias, shared, residual, y,
                                                                   out_dtype, None, norm, experts, **gate))
         if norm is not None:
             weight, eps = norm
