@@ -2,8 +2,8 @@
 // straight to the C ABI: tensors are looked at through torch's C++ interface,
 // new outputs come from its allocator, and the library's function runs on the
 // current stream. Every function returns None for anything that is not such a
-// call (a wrong type, shape, device or distance, a gradient that would be
-// lost, a status that is not 0), and the Python function of the same name then
+// call (a wrong type, shape, device or distance, a gradient or tangent that would
+// be lost, a status that is not 0), and the Python function of the same name then
 // goes through its own checks, which say what is wrong. (Host time of a call
 // of linear_fp8 through ctypes 9.6 us, so 5; the smallest kernels take 3.)
 #define PY_SSIZE_T_CLEAN
@@ -55,7 +55,8 @@ struct Call {
         if (!ok || !THPVariable_Check(o)) return no();
         const Tensor& t = THPVariable_Unpack(o);
         if (!t.defined() || !t.is_cuda() || t.unsafeGetTensorImpl()->is_python_dispatch() ||
-            t.layout() != c10::kStrided || (t.requires_grad() && c10::GradMode::is_enabled()))
+            t.layout() != c10::kStrided || (t.requires_grad() && c10::GradMode::is_enabled()) ||
+            t._fw_grad(0).defined())   // a forward-mode tangent
             return no();
         if (dev < 0) {
             dev = t.device().index();

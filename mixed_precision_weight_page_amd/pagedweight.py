@@ -17,6 +17,7 @@ from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 # PW_LIBRARY may name another build of the same library (the tests' host
 # sanitizer build); by default the one built in-tree
@@ -240,6 +241,9 @@ def _on_gpu(t, dev: int, name: str):
     if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, but this call is forward only: detach it, "
                          "or call under torch.no_grad()")
+    if _forward_ad._current_level >= 0 and isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} carries a forward-mode tangent, which this call would drop: "
+                         "pass torch.autograd.forward_ad.unpack_dual(...).primal")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.get_device() != dev:
