@@ -1053,7 +1053,8 @@ hipError_t launch_grouped_any_size(const ProductArgs& a, hipStream_t s) {
     if (!a.aligned) return launch_any<T, GLU, true>(a, s);
     if (mean > 16) return launch_tiles<T, GLU, true>(a, choose_tile<T, GLU, true>(a).tile, s);
     if (mean > 8) return launch_stream<T, 2, 2, 2, GLU, true>(a, waves, s);
-    if (!kEight<T> && waves == 4) return launch_stream<T, 4, 1, 2, GLU, true>(a, 4, s);
+    if constexpr (!kEight<T>)
+        if (waves == 4) return launch_stream<T, 4, 1, 2, GLU, true>(a, 4, s);
     return launch_stream<T, 2, 1, 2, GLU, true>(a, waves, s);
 }
 

@@ -39,7 +39,7 @@ def kernels(tmp_path_factory):
 
 def test_nothing_is_cut_off_or_kept_in_scratch(kernels):
     products = {n: seq for n, seq in kernels.items() if "mfma" in seq or "mfma8" in seq}
-    assert len(products) == 2 * (4 + 2 + 4 + 1) + 2 * (4 + 2 + 3) - 1   # with SwiGLU no block of 16 weight rows alone
+    assert len(products) == 2 * (4 + 2 + 4 + 1) + 2 * (4 + 2 + 2) - 1   # with SwiGLU no block of 16 weight rows alone
     for name, seq in products.items():
         assert "mfma8" not in seq and "scratch" not in seq, name
 
