@@ -346,13 +346,15 @@ typedef struct {
  * ceil(N / 128) rows; with SWIGLU ceil(N / 128) for the gate rows, then as
  * many for the up rows (each half's tiles from its own first row). Distances
  * of scales may be 0; a product's scales (256 rows of x, all of w's rows, all
- * blocks of columns) lie within 2^31 bytes. Sums and scales are fp32. An fp32
- * y comes from exact products, on 16-bit matrix instructions; for a 16-bit y
- * the 8-bit ones, which are twice as fast, cut a product off at 2^-13 of the
- * power of two under the largest of its eight neighbours along K (columns
- * 8 i .. 8 i + 7): about 1.5e-5 of the result's norm for normally distributed
- * operands, 3.5e-5 where a few channels are twenty times the others, beside up to
- * 2^-9 of each value (bf16; fp16 2^-12) that the rounding of y takes. Rows of any
+ * blocks of columns) lie within 2^31 bytes. Sums and scales are fp32 (so is xs ws,
+ * which therefore has to be in its range). An fp32 y comes from exact products,
+ * on 16-bit matrix instructions. For a 16-bit y the 8-bit ones, which are twice
+ * as fast, cut each product off, towards zero, at 2^(E - 13): E is the largest
+ * sum of the two codes' exponents (-6 below 2^-6) among the products, not zero,
+ * of its eight neighbours along K (columns 8 i .. 8 i + 7). That is about 1.5e-5
+ * of the result's norm for normally distributed operands and 3.5e-5 where a few
+ * channels are twenty times the others, beside up to 2^-8 (bf16; fp16 2^-11) of
+ * each value that the rounding of y takes. Rows of any
  * alignment and length (16-byte aligned ones, with K a multiple of 16, are
  * faster). Else as pw_linear. */
 pw_status pw_linear_fp8(const pw_linear_fp8_desc* desc, const void* x, const float* x_scale, const void* w,

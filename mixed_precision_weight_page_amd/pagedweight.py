@@ -545,8 +545,9 @@ def linear_fp8(x: Fp8, w: Fp8, bias: Optional[torch.Tensor] = None, act: str = "
     [ceil(N / 128), ceil(K / 128)] (quantize_fp8 with block "tile"); with act
     "swiglu" codes [2 N, K] and the gate's scale rows, then the up half's.
     out_dtype: default y's or residual's type, else bfloat16. A float32 y is
-    summed from exact products, a 16-bit one from products to 2^-13 of the
-    largest of their eight neighbours along K, in half the time. Else as linear."""
+    summed from exact products; for a 16-bit one the matrix cores keep them to
+    about 2^-13 of the largest of eight neighbours along K, in half the time.
+    Else as linear."""
     if stream is None and _fast is not None:
         got = _fast.linear_fp8(x, w, bias, ACTIVATIONS.get(act), residual, y, out_dtype)
         if got is not None:
@@ -702,7 +703,9 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, g: torch.Tensor, w_gate_up: 
     d] and w_down [E, d, F] of x's type, or both Fp8 with scales for 128 x 128
     tiles (x and the SwiGLU rows are then quantized by rows). group_routes, two
     grouped_linear, join_routes. Rounded on the way: the SwiGLU rows to x's type
-    (and to e4m3), each pair's product to x's type unless y is float32.
+    (and to e4m3), each pair's product to x's type unless y is float32. x has
+    less than 2^31 - 64 bytes (8-bit weights: elements), as grouped_linear
+    gathers its rows.
     out_dtype: default y's, residual's or x's type."""
     side = _other_stream(stream)
     if side is not None:

@@ -144,3 +144,38 @@ def test_experts_with_an_fp32_result(T):
     # k products and sums, each off by half a step of a sum of at most `size`
     tol = tol + (k + 1) * 2.0 ** -23 * (size + tol)
     assert bool(((y - want).abs() <= tol).all()), float(((y - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("M,N,pad", [(254, 1, 0), (254, 1, 3), (254, 300, 0), (254, 5000, 0), (2540, 3000, 0), (2540, 3000, 1)])
+def test_every_code_by_one(M, N, pad):
+    """K = 1: y is the code's own value, for each of the finite ones."""
+    from mixed_precision_weight_page_amd import linear_fp8
+    codes = torch.arange(256, dtype=torch.uint8).view(E4M3)
+    fine = codes[(torch.arange(256) & 127) != 127]
+    x = fine.view(torch.uint8).repeat(M // 254)[:, None].view(E4M3)
+    w = torch.ones(N, 1).to(E4M3)
+    one = torch.ones((), device="cuda")
+    for K in (1, 16):   # the others are zeros
+        xk, wk = torch.zeros(M, K).to(E4M3), torch.zeros(N, K).to(E4M3)
+        xk[:, :1], wk[:, :1] = x, w
+        y = linear_fp8((strided(xk, pad), one.expand(M, 1)), (strided(wk, pad), one.expand(-(-N // 128), 1)), out_dtype=torch.float32)
+        assert torch.equal(y.cpu(), x.float().expand(M, N))
+
+
+@pytest.mark.parametrize("M", [5, 60, 200, 3000])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_infinities_and_nans_stay_in_their_rows(M, pad):
+    from mixed_precision_weight_page_amd import grouped_linear, linear_fp8
+    gen = torch.Generator().manual_seed(M)
+    for N in (130, 2000):
+        x, (xq, xs) = eight_bits((M, 272), gen, False)
+        w, (wq, ws) = eight_bits((N, 272), gen, True, pad=pad)
+        xq, xs = xq.float().cpu(), xs.cpu().clone()
+        xq[2, 0], xs[3, 1], xs[4, 0] = float("nan"), float("inf"), float("nan")
+        xd = (strided(xq.to(E4M3), pad), xs.t().contiguous().cuda().t())
+        off = torch.tensor([0, M // 2, M], dtype=torch.int32).cuda()
+        for y in (linear_fp8(xd, (wq, ws), out_dtype=torch.float32),
+                  grouped_linear(xd, off, (torch.stack([wq, wq]), torch.stack([ws, ws])), out_dtype=torch.float32)):
+            y = y.cpu()
+            assert bool(y[2].isnan().all()) and bool(y[4].isnan().all()) and not bool(y[3].isfinite().any())
+            assert bool(y[[i for i in range(M) if i not in (2, 3, 4)]].isfinite().all())
